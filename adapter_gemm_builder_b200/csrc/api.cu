@@ -114,6 +114,86 @@ size_t bwd_ws_layout(int M, const lora_pool_t* pool, size_t* off_at, size_t* off
     return off;
 }
 
+// Planes of v that the shrink of a batch writes: the tensor-core shrink's for long
+// segments, one otherwise.
+int shrink_planes(int T, const lora_pool_t& pool) { return sgmv_expand_tc_eligible(T, pool) ? sgmv_shrink_tc_parts(pool) : 1; }
+
+// The pool whose A and B are the transposes (h_in and h_out swapped), for the backward.
+lora_pool_t transposed(const lora_pool_t& pool, void* At, void* Bt)
+{
+    lora_pool_t t = pool;
+    t.A = At;
+    t.B = Bt;
+    t.h_in = pool.h_out;
+    t.h_out = pool.h_in;
+    return t;
+}
+
+// Gated forward workspace: status | planes of v | operands | adapter lists (adapters only).
+struct GatedWs {
+    size_t v, ops, lists, size;
+};
+GatedWs gated_ws(int M, const lora_pool_t* pool)
+{
+    GatedWs w = {};
+    w.size = 256;
+    if (!pool) return w;
+    w.v = w.size;
+    w.size += align256(apply_v_bytes(M, *pool, shrink_planes(M, *pool)));
+    w.ops = w.size;
+    w.size += align256(gated_operand_bytes(M, pool->r_max));
+    w.lists = w.size;
+    w.size += align256(gated_list_bytes(M));
+    return w;
+}
+
+// Gated backward workspace: status | dg, du | with adapters: x expanded | A' = B^T, B' = A^T of
+// both slices | planes of u, then of v | operands of u, of v | adapter lists.
+struct GatedBwdWs {
+    size_t d, x, at, bt, v, ops_u, ops_v, lists, size;
+};
+GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
+{
+    GatedBwdWs w = {};
+    w.size = 256;
+    w.d = w.size;
+    w.size += align256((size_t)2 * M * F * 2);
+    if (!pool) return w;
+    const size_t na = (size_t)pool->n_adapters;
+    w.x = w.size;
+    w.size += align256((size_t)M * pool->h_in * 2);
+    w.at = w.size;
+    w.size += align256(2 * na * F * pool->r_max * 2);
+    w.bt = w.size;
+    w.size += align256(2 * na * pool->r_max * pool->h_in * 2);
+    w.v = w.size;
+    const lora_pool_t t = transposed(*pool, nullptr, nullptr);
+    const size_t a = apply_v_bytes(M, *pool, shrink_planes(M, *pool)), b = apply_v_bytes(M, t, shrink_planes(M, t));
+    w.size += align256(a > b ? a : b);
+    w.ops_u = w.size;
+    w.size += align256(gated_operand_bytes(M, pool->r_max));
+    w.ops_v = w.size;
+    w.size += align256(gated_operand_bytes(M, pool->r_max));
+    w.lists = w.size;
+    w.size += align256(gated_list_bytes(M));
+    return w;
+}
+
+// v = x.A of both slices into planes at v, then its operands and the tiles' adapter lists.
+cudaError_t gated_operands(const void* x, int64_t x_slice_stride, const lora_pool_t& pool, const lora_segments_t& seg,
+                           int M, float* v, void* ops, void* lists, cudaStream_t s)
+{
+    int planes = shrink_planes(M, pool);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (planes > 1 || sgmv_expand_tc_eligible(M, pool)) e = launch_sgmv_shrink_tc(x, x_slice_stride, pool, seg, v, planes, s);
+    if (e == cudaErrorInvalidValue) {  // short segments, or the pool's tensor map was refused
+        planes = 1;
+        e = launch_sgmv(SGMV_SHRINK, x, x_slice_stride, pool, seg, v, nullptr, s, false);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_gated_operands(v, planes, pool, seg, M, ops, lists, s);
+}
+
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
 std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitNs};
 std::atomic<int> g_inject_stall{0};
@@ -313,6 +393,14 @@ size_t lora_workspace_size(int op, int T, int K, const lora_pool_t* pool)
         size_t a, b, c, d;
         return bwd_ws_layout(T, pool, &a, &b, &c, &d);
     }
+    case LORA_OP_BF16_GATED:
+        if (T < 1 || K <= 0 || (pool && (check_pool(pool) != LORA_OK || pool->n_slices != 2 || pool->h_in != K)))
+            return (size_t)-1;
+        return gated_ws(T, pool).size;
+    case LORA_OP_BF16_GATED_BACKWARD:
+        if (T < 1 || K <= 0 || (pool && (check_pool(pool) != LORA_OK || pool->n_slices != 2 || pool->h_out != K)))
+            return (size_t)-1;
+        return gated_bwd_ws(T, K, pool).size;
     case LORA_OP_FP8_GEMM:
     case LORA_OP_BF16_GEMM:
     case LORA_OP_MXFP4_GEMM:
@@ -526,6 +614,155 @@ int fp8_lora_backward(const void* x, const void* dY, int M, int K, int N, const 
     if (launch_sgmv(SGMV_SHRINK, x, 0, *pool, *seg, v, nullptr, s, false) != cudaSuccess ||
         launch_grad_outer(true, x, u, K, *pool, *seg, dA, s) != cudaSuccess ||
         launch_grad_outer(false, dY, v, N, *pool, *seg, dB, s) != cudaSuccess)
+        return LORA_ERR_CUDA;
+    return LORA_OK;
+}
+
+static bool act8_ok(const lora_act8_t* a) { return a && a->codes && a->scales && aligned16(a->codes); }
+
+int act8_compress_rows(const void* x, int M, int N, const lora_act8_t* out, lora_stream_t stream)
+{
+    if (M < 0 || N < 16 || N % 16) return LORA_ERR_INVALID_ARG;
+    if (M == 0) return LORA_OK;
+    if (!x || !aligned16(x) || !act8_ok(out)) return LORA_ERR_INVALID_ARG;
+    if ((long long)M * ((N + 255) / 256) >= (1ll << 31)) return LORA_ERR_UNSUPPORTED;
+    return cuda_status(launch_act8_compress(x, M, N, *out, (cudaStream_t)stream));
+}
+
+int act8_expand_rows(const lora_act8_t* in, int M, int N, void* x, lora_stream_t stream)
+{
+    if (M < 0 || N < 16 || N % 16) return LORA_ERR_INVALID_ARG;
+    if (M == 0) return LORA_OK;
+    if (!x || !aligned16(x) || !act8_ok(in)) return LORA_ERR_INVALID_ARG;
+    if ((long long)M * ((N + 255) / 256) >= (1ll << 31)) return LORA_ERR_UNSUPPORTED;
+    return cuda_status(launch_act8_expand(*in, M, N, x, (cudaStream_t)stream));
+}
+
+// Checks that the gated block's forward and backward share.
+static int gated_check(int M, int K, int F, const void* Wg, const void* Wu, int act, const lora_pool_t* pool,
+                       const lora_segments_t* seg)
+{
+    if (M < 1 || K < 8 || F < 8 || K % 8 || F % 8) return LORA_ERR_INVALID_ARG;
+    if (!Wg || !Wu || !aligned16(Wg) || !aligned16(Wu)) return LORA_ERR_INVALID_ARG;
+    if (act != LORA_ACT_SILU && act != LORA_ACT_GELU) return LORA_ERR_INVALID_ARG;
+    if (M > (1 << 24)) return LORA_ERR_UNSUPPORTED;
+    if (pool) {
+        int st = check_pool(pool);
+        if (st != LORA_OK) return st;
+        if (pool->n_slices != 2 || pool->h_in != K || pool->h_out != F) return LORA_ERR_INVALID_ARG;
+        if ((st = check_segments(seg, pool->n_adapters)) != LORA_OK) return st;
+        if (seg->T != M) return LORA_ERR_INVALID_ARG;
+    }
+    return LORA_OK;
+}
+
+int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void* Wg, const void* Wu, int act,
+                                  const lora_pool_t* pool, const lora_segments_t* seg, void* h, const lora_act8_t* g8,
+                                  const lora_act8_t* u8, void* ws, size_t ws_bytes, lora_stream_t stream)
+{
+    const int st = gated_check(M, K, F, Wg, Wu, act, pool, seg);
+    if (st != LORA_OK) return st;
+    if (!x || !h || !aligned16(x) || !aligned16(h)) return LORA_ERR_INVALID_ARG;
+    if ((g8 == nullptr) != (u8 == nullptr)) return LORA_ERR_INVALID_ARG;
+    if (g8 && (F % 16 || !act8_ok(g8) || !act8_ok(u8))) return LORA_ERR_INVALID_ARG;
+    const GatedWs l = gated_ws(M, pool);
+    if (!ws || ws_bytes < l.size || !aligned16(ws)) return LORA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    GatedGemmArgs a = {};
+    a.M = M;
+    a.K = K;
+    a.F = F;
+    a.act = act;
+    a.a[0] = x;
+    a.W[0] = Wg;
+    a.W[1] = Wu;
+    a.out = h;
+    a.g8 = g8;
+    a.u8 = u8;
+    a.status = reinterpret_cast<uint32_t*>(w);
+    if (pool) {
+        if (gated_operands(x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
+            return LORA_ERR_CUDA;
+        a.lora = true;
+        a.ops = w + l.ops;
+        a.lists = w + l.lists;
+        a.B = pool->B;
+        a.tok_adapter = seg->tok_adapter;
+        a.ranks = pool->ranks;
+        a.n_adapters = pool->n_adapters;
+        a.r_max = pool->r_max;
+    }
+    return cuda_status(launch_gated_gemm(a, s));
+}
+
+int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* dh, int M, int K, int F, const void* Wg,
+                             const void* Wu, int act, const lora_pool_t* pool, const lora_segments_t* seg,
+                             const lora_act8_t* g8, const lora_act8_t* u8, void* h, void* dX, void* dA, void* dB, void* ws,
+                             size_t ws_bytes, lora_stream_t stream)
+{
+    const int st = gated_check(M, K, F, Wg, Wu, act, pool, seg);
+    if (st != LORA_OK) return st;
+    if (F % 16 || !dh || !dX || !aligned16(dh) || !aligned16(dX) || !aligned16(h)) return LORA_ERR_INVALID_ARG;
+    if (!act8_ok(g8) || !act8_ok(u8)) return LORA_ERR_INVALID_ARG;
+    if ((long long)M * ((F + 255) / 256) >= (1ll << 31)) return LORA_ERR_UNSUPPORTED;
+    if (pool) {
+        if ((x == nullptr) == (x8 == nullptr) || !dA || !dB) return LORA_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(dA) || !aligned16(dB)) return LORA_ERR_INVALID_ARG;
+        if (x8 && (K % 16 || !act8_ok(x8))) return LORA_ERR_INVALID_ARG;
+        if ((long long)M * ((K + 255) / 256) >= (1ll << 31)) return LORA_ERR_UNSUPPORTED;
+    }
+    const GatedBwdWs l = gated_bwd_ws(M, F, pool);
+    if (!ws || ws_bytes < l.size || !aligned16(ws)) return LORA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    uint16_t* dg = reinterpret_cast<uint16_t*>(w + l.d);
+    uint16_t* du = dg + (size_t)M * F;
+    // 1. dg, du (and h) from the checkpoints
+    if (launch_gated_point(dh, M, F, act, *g8, *u8, dg, du, h, s) != cudaSuccess) return LORA_ERR_CUDA;
+    GatedGemmArgs a = {};
+    a.backward = true;
+    a.M = M;
+    a.K = K;
+    a.F = F;
+    a.a[0] = dg;
+    a.a[1] = du;
+    a.W[0] = Wg;
+    a.W[1] = Wu;
+    a.out = dX;
+    a.status = reinterpret_cast<uint32_t*>(w);
+    if (!pool) return cuda_status(launch_gated_gemm(a, s));
+    // 2. the transposed pools of the active adapters (A' = B^T, B' = A^T) and u = d.A'
+    const size_t na = (size_t)pool->n_adapters, at = na * F * pool->r_max, bt = na * pool->r_max * K;
+    lora_pool_t pt = transposed(*pool, w + l.at, w + l.bt);
+    float* v = reinterpret_cast<float*>(w + l.v);
+    for (int i = 0; i < 2; ++i) {
+        lora_pool_t one = *pool;
+        one.A = static_cast<const uint16_t*>(pool->A) + i * bt;
+        one.B = static_cast<const uint16_t*>(pool->B) + i * at;
+        if (launch_transpose_pool(one, *seg, reinterpret_cast<uint16_t*>(w + l.at) + i * at,
+                                  reinterpret_cast<uint16_t*>(w + l.bt) + i * bt, s) != cudaSuccess)
+            return LORA_ERR_CUDA;
+    }
+    if (gated_operands(dg, (int64_t)M * F, pt, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+    // 3. dX, the adapters' term in its sum
+    a.lora = true;
+    a.ops = w + l.ops_u;
+    a.lists = w + l.lists;
+    a.B = pt.B;
+    a.tok_adapter = seg->tok_adapter;
+    a.ranks = pool->ranks;
+    a.n_adapters = pool->n_adapters;
+    a.r_max = pool->r_max;
+    if (launch_gated_gemm(a, s) != cudaSuccess) return LORA_ERR_CUDA;
+    // 4. v = x.A, then the adapters' gradients
+    if (x8) {
+        if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
+        x = w + l.x;
+    }
+    if (gated_operands(x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
+        launch_gated_outer(true, x, 0, K, w + l.ops_u, M, *pool, *seg, dA, s) != cudaSuccess ||
+        launch_gated_outer(false, dg, (int64_t)M * F, F, w + l.ops_v, M, *pool, *seg, dB, s) != cudaSuccess)
         return LORA_ERR_CUDA;
     return LORA_OK;
 }

@@ -1,0 +1,650 @@
+// gated.cu -- the gated feed-forward block's matrix products on the tcgen05 tensor cores
+// (TMA in, accumulators in TMEM), with the multi-tenant LoRA term of both projections:
+//
+//   forward   g = x.Wg^T + s_a (x.A0_a).B0_a,  u = x.Wu^T + s_a (x.A1_a).B1_a,
+//             h = bf16(act(g) u), and on request g, u as 8-bit checkpoints (act8.cuh);
+//   backward  dX = dg.Wg + du.Wu + s_a (dg.B0_a^T).A0_a^T + s_a (du.B1_a^T).A1_a^T.
+//
+// One kernel, two modes. A tile is 128 tokens (the MMA's M) by up to 256 accumulator
+// columns. Forward: the columns are bnh of gate and the same bnh of up, so one MMA per 16 of
+// K computes both and the thread that drains a row finds g and u of the same element in the
+// same TMEM lane: the activation and the product need no exchange, and a block of 32 columns
+// (one checkpoint scale) lies in one thread. Backward: the sum runs over dg then du (2F long),
+// and Wg, Wu [F][K] are read as they are, as the MMA's MN-major operand (no transposed copy).
+//
+// The LoRA term extends the sum of a tile: for every adapter that has tokens among the tile's
+// 128 rows (listed by operand_kernel below, in order of first appearance) one more ring stage per
+// slice holds v (the rows of other adapters zero) against B_a's rows. v comes as bf16 halves
+// hi + lo in the forward (about 16 bits of v: a checkpoint's codes must not flip by the
+// rounding of v) and as hi alone in the backward, whose dg and du are bf16 already. Tokens
+// stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens are sorted
+// by adapter has few adapters per tile.
+//
+// Roles (448 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
+// chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..13 build
+// the LoRA stages. Two accumulators (512 TMEM columns), so a tile drains under the next one's
+// products. Every wait is bounded; on expiry the CTA records a status word, lets what it
+// issued land and leaves.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "act8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "sgmv_common.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kGDrainWarps = 8;
+constexpr int kGProducer = kGDrainWarps, kGMma = kGProducer + 1, kGBuilder0 = kGMma + 1;
+constexpr int kGBuilders = 128;
+constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
+constexpr int kGTileM = 128;
+constexpr int kGMaxStages = 8;
+constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
+constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
+constexpr int kGBarBytes = 512;
+constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
+enum { kGFwd = 0, kGBwd = 1 };
+// status bits of the bounded waits
+enum { kGStRing = 0x1, kGStMma = 0x2, kGStBuild = 0x4, kGStDrain = 0x8, kGStStall = 0x10 };
+
+struct GatedParams {
+    int M, NC;        // tokens; output columns (F forward, K backward)
+    int mt, tiles;    // token tiles, all tiles
+    int bn, cols;     // accumulator columns of a tile; output columns of a tile (bn / 2 forward)
+    int kb, kb_half;  // ring stages of a tile's main sum; backward: those of dg
+    int stages, stage_bytes, a_bytes;
+    int act;
+    uint16_t* out;    // h [M][F] or dX [M][K]
+    uint8_t *g_codes, *g_scales, *u_codes, *u_scales;  // forward checkpoints or NULL
+    uint32_t* status;
+    unsigned long long timeout_ns;
+    int inject_stall;
+    // LoRA
+    const uint16_t* ops;      // [2][M][hi r16 | lo r16]: s_a v as bf16 halves
+    const uint16_t* B;        // [2][n_adapters][r_max][NC]
+    const int32_t* lists;     // [mt][128] adapters of a token tile
+    const int32_t* list_len;  // [mt]
+    const int32_t* tok_adapter;
+    const int32_t* ranks;
+    int n_adapters, r_max, r16;
+};
+
+// K-major operand, 128-byte rows, 128-byte swizzle: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t g_desc_k(uint32_t a)
+{
+    return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+// MN-major operand in 64-column boxes of 128-byte rows (one per k), 128-byte swizzle, boxes
+// `atom` bytes apart.
+__device__ __forceinline__ uint64_t g_desc_mn(uint32_t a, uint32_t atom)
+{
+    return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)((atom >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, bf16 operands, fp32 accumulator, M = 128, N = n; B MN-major or K-major.
+__device__ __forceinline__ uint32_t g_idesc(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// act(g): x sigmoid(x), or x Phi(x) through the complementary error function (no
+// cancellation in the lower tail).
+__device__ __forceinline__ float gate(int act, float g)
+{
+    if (act == LORA_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
+    return 0.5f * g * erfcf(g * -0.70710678118654752f);
+}
+
+__device__ __forceinline__ void store_bf16x8(uint16_t* dst, const float* v)
+{
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                                pack_bf16x2(v[6], v[7]));
+}
+
+// One thread's block of 32 accumulator columns as a checkpoint block; columns past the row's
+// end hold zeros and are not stored (n: 32 or 16 live columns).
+__device__ __forceinline__ void save_block(const float* v, int n, uint8_t* codes, uint8_t* scale)
+{
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, act8::finite(v[i]) ? fabsf(v[i]) : 0.f);
+    const uint32_t E = act8::scale_code(top);
+    const float inv = act8::inv_scale(E);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* w = v + h * 16 + i * 4;
+            o[i] = (uint32_t)ptx::cvt_e4m3x2(act8::scaled(w[0], inv), act8::scaled(w[1], inv)) |
+                   ((uint32_t)ptx::cvt_e4m3x2(act8::scaled(w[2], inv), act8::scaled(w[3], inv)) << 16);
+        }
+        if (h * 16 < n) *reinterpret_cast<uint4*>(codes + h * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    *scale = (uint8_t)E;
+}
+
+template <int MODE, bool LORA>
+__global__ void __launch_bounds__(kGThreads, 1)
+gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GatedParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw_u = ptx::smem_u32(smem_raw);
+    const uint32_t base_u = (raw_u + 1023u) & ~1023u;
+    uint8_t* ring = smem_raw + (base_u - raw_u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + kGSmem - kGBarBytes);
+    uint64_t* empty = full + kGMaxStages;
+    uint64_t* go = empty + kGMaxStages;  // the stage is free for the builders
+    uint64_t* tfull = go + kGMaxStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mdone = tempty + 2;
+    uint64_t* stall = mdone + 1;  // test hook: never completed
+    volatile int* abort_flag = &s_abort;
+    int32_t* status = reinterpret_cast<int32_t*>(p.status);
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < kGMaxStages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&go[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], kGDrainWarps);
+        }
+        ptx::mbar_init(mdone, 1);
+        ptx::mbar_init(stall, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == kGMma) {
+        ptx::tmem_alloc(&s_tmem, 2 * kGAccCols);
+        ptx::tmem_relinquish();
+    }
+    // Without adapters the operands may come from the kernel before this one. With them that
+    // kernel is operand_kernel, which let this one start only after all that ran before it was
+    // complete: x, dg, du and the weights may be read at once, its own outputs after the wait.
+    if (!LORA) ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp == kGProducer) {
+        // ================================================================ producer
+        if (lane == 0) {
+            int st = 0;
+            uint32_t use = 0;            // uses of stage st before this one (all stages below st: one more)
+            int last[kGMaxStages];       // parity of the stage's last TMA fill, -1 if a builder filled it last
+            for (int s = 0; s < kGMaxStages; ++s) last[s] = -1;
+            bool ok = true;
+            if (p.inject_stall && blockIdx.x == 0)  // test hook: a wait that runs out
+                ok = wait_one<false>(stall, 0, abort_flag, status, kGStStall, p.timeout_ns);
+            auto acquire = [&]() {
+                return use == 0 || wait_one<false>(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
+            };
+            auto next = [&]() {
+                if (++st == p.stages) {
+                    st = 0;
+                    ++use;
+                }
+            };
+            bool waited = !LORA;
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+                const int m = t % p.mt, n0 = (t / p.mt) * p.cols;
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!(ok = acquire())) break;
+                    const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+                    ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(p.a_bytes + p.bn * 128));
+                    last[st] = (int)(use & 1);
+                    if (MODE == kGFwd) {
+                        ptx::tma_load_2d(sa, &tmA0, &full[st], kb * kGKBlock, m * kGTileM);
+                        ptx::tma_load_2d(sb, &tmB0, &full[st], kb * kGKBlock, n0);
+                        ptx::tma_load_2d(sb + (uint32_t)(p.cols * 128), &tmB1, &full[st], kb * kGKBlock, n0);
+                    } else {
+                        const bool up = kb >= p.kb_half;
+                        const int f0 = (up ? kb - p.kb_half : kb) * kGKBlock;
+                        ptx::tma_load_2d(sa, up ? &tmA1 : &tmA0, &full[st], f0, m * kGTileM);
+                        for (int b = 0; b < p.bn / 64; ++b)
+                            ptx::tma_load_2d(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, &full[st], n0 + b * 64, f0);
+                    }
+                    next();
+                }
+                if (LORA && ok) {
+                    if (!waited) ptx::pdl_wait();
+                    waited = true;
+                    for (int e = 2 * p.list_len[m]; e > 0; --e) {
+                        if (!(ok = acquire())) break;
+                        last[st] = -1;
+                        ptx::mbar_arrive(&go[st]);
+                        next();
+                    }
+                }
+            }
+            if (!ok)  // let every copy this CTA issued land before it leaves
+                for (int s = 0; s < p.stages; ++s)
+                    if (last[s] >= 0)
+                        wait_one<false, false>(&full[s], (uint32_t)last[s], abort_flag, status, kGStRing, p.timeout_ns);
+        }
+    } else if (warp == kGMma) {
+        // ================================================================ MMA issuer
+        if (lane == 0) {
+            int st = 0, acc = 0;
+            uint32_t use = 0;
+            bool ok = true, waited = !LORA;
+            auto next = [&]() {
+                if (++st == p.stages) {
+                    st = 0;
+                    ++use;
+                }
+            };
+            const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, true);
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++acc) {
+                const int m = t % p.mt, buf = acc & 1;
+                if (acc >= 2 &&
+                    !(ok = wait_one<false>(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
+                                           p.timeout_ns)))
+                    break;
+                const uint32_t d = tmem + (uint32_t)(buf * kGAccCols);
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        ptx::tc_mma_f16(d, g_desc_k(sa + (uint32_t)(ks * 32)),
+                                        MODE == kGFwd ? g_desc_k(sb + (uint32_t)(ks * 32))
+                                                      : g_desc_mn(sb + (uint32_t)(ks * 2048), 8192),
+                                        id_main, (kb | ks) ? 1u : 0u);
+                    ptx::tc_commit(&empty[st]);
+                    next();
+                }
+                if (LORA && ok) {
+                    if (!waited) ptx::pdl_wait();
+                    waited = true;
+                    const int ext = 2 * p.list_len[m];
+                    for (int e = 0; e < ext; ++e) {
+                        if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+                        ptx::tc_fence_after();
+                        const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes);
+                        const int halves = MODE == kGFwd ? 2 : 1;
+                        const uint32_t sb = sa + (uint32_t)(halves * p.a_bytes);
+                        const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
+                        for (int h = 0; h < halves; ++h)
+                            for (int ks = 0; ks < (p.r16 >> 4); ++ks)
+                                ptx::tc_mma_f16(ds, g_desc_k(sa + (uint32_t)(h * p.a_bytes + ks * 32)),
+                                                g_desc_mn(sb + (uint32_t)(ks * 2048), (uint32_t)(p.r16 * 128)), id_lora, 1u);
+                        ptx::tc_commit(&empty[st]);
+                        next();
+                    }
+                }
+                if (ok) ptx::tc_commit(&tfull[buf]);
+            }
+            // every MMA issued is complete before the CTA leaves
+            ptx::tc_commit(mdone);
+            wait_one<false, false>(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns);
+        }
+    } else if (warp >= kGBuilder0) {
+        // ================================================================ LoRA stages
+        if (LORA) {
+            ptx::pdl_wait();
+            const int bt = threadIdx.x - kGBuilder0 * 32;
+            const int chunks = p.r16 >> 3, bpr = p.cols >> 3;  // 16-byte chunks of an operand row, of a B row
+            const int halves = MODE == kGFwd ? 2 : 1;
+            int st = 0;
+            uint32_t gos[kGMaxStages];  // fills of stage s so far
+            for (int s = 0; s < kGMaxStages; ++s) gos[s] = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+                const int m = t % p.mt, n0 = (t / p.mt) * p.cols, row = m * kGTileM + bt;
+                const int mine = row < p.M ? p.tok_adapter[row] : -1;
+                const int len = p.list_len[m];
+                st = (st + p.kb) % p.stages;
+                for (int e = 0; e < 2 * len && ok; ++e) {
+                    const int a = p.lists[m * kGTileM + (e >> 1)], s = e & 1;
+                    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+                    uint32_t par = 0;
+#pragma unroll
+                    for (int i = 0; i < kGMaxStages; ++i)
+                        if (i == st) par = gos[i]++ & 1;
+                    // all builders take part or none (a wait that ran out may show in one warp only)
+                    ok = wait_all<false>(&go[st], par, abort_flag, status, kGStBuild, p.timeout_ns);
+                    ok = !ptx::named_sync_or(1, kGBuilders, !ok);
+                    if (!ok) break;
+                    uint8_t* sa = ring + st * p.stage_bytes;
+                    // v: this thread's row, zero for tokens of other adapters
+                    if (bt * 128 < p.a_bytes) {
+                        const uint4* src = reinterpret_cast<const uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
+                        for (int h = 0; h < halves; ++h)
+                            for (int c = 0; c < chunks; ++c)
+                                *reinterpret_cast<uint4*>(sa + h * p.a_bytes + bt * 128 + ((c ^ (bt & 7)) << 4)) =
+                                    mine == a ? src[h * chunks + c] : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    // B_a's rows of these columns, zero past the rank and past the row's end
+                    uint8_t* sb = sa + halves * p.a_bytes;
+                    const uint16_t* Ba = p.B + ((size_t)s * p.n_adapters + a) * p.r_max * p.NC + n0;
+                    for (int i = bt; i < p.r16 * bpr; i += kGBuilders) {
+                        const int j = i / bpr, c = i - j * bpr;
+                        const bool in = j < r && n0 + c * 8 < p.NC;
+                        *reinterpret_cast<uint4*>(sb + (c >> 3) * (p.r16 * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
+                            in ? *reinterpret_cast<const uint4*>(Ba + (size_t)j * p.NC + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    ptx::named_sync(2, kGBuilders);
+                    if (bt == 0) ptx::mbar_arrive(&full[st]);
+                    if (++st == p.stages) st = 0;
+                }
+            }
+        }
+    } else {
+        // ================================================================ drain
+        const int q = warp & 3, half = warp >> 2;
+        int acc = 0;
+        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++acc) {
+            const int m = t % p.mt, n0 = (t / p.mt) * p.cols, buf = acc & 1;
+            const int row = m * kGTileM + q * 32 + lane;
+            if (!wait_all<false>(&tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status, kGStDrain, p.timeout_ns)) break;
+            ptx::tc_fence_after();
+            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGAccCols);
+            if (m * kGTileM + q * 32 < p.M) {  // the warp has live rows
+                if (MODE == kGFwd && p.g_codes) {
+                    const int nb = (p.NC + act8::kBlock - 1) / act8::kBlock;
+                    for (int c = half * 32; c < p.cols; c += 64) {
+                        const int col = n0 + c;
+                        if (col >= p.NC) break;
+                        float g[32], u[32];
+                        ptx::tmem_ld32(ta + (uint32_t)c, g);
+                        ptx::tmem_ld32(ta + (uint32_t)(p.cols + c), u);
+                        if (row < p.M) {
+                            const int live = min(32, p.NC - col);
+                            const size_t at = (size_t)row * p.NC + col, sc = (size_t)row * nb + (col >> 5);
+                            save_block(g, live, p.g_codes + at, p.g_scales + sc);
+                            save_block(u, live, p.u_codes + at, p.u_scales + sc);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) g[i] = gate(p.act, g[i]) * u[i];
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                if (i < live) store_bf16x8(p.out + at + i, g + i);
+                        }
+                    }
+                } else {
+                    for (int c = half * 16; c < p.cols; c += 32) {
+                        const int col = n0 + c;
+                        if (col >= p.NC) break;
+                        float g[16], u[16];
+                        ptx::tmem_ld16(ta + (uint32_t)c, g);
+                        if (MODE == kGFwd) {
+                            ptx::tmem_ld16(ta + (uint32_t)(p.cols + c), u);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) g[i] = gate(p.act, g[i]) * u[i];
+                        }
+                        if (row < p.M) {
+                            uint16_t* o = p.out + (size_t)row * p.NC + col;
+                            store_bf16x8(o, g);
+                            if (col + 8 < p.NC) store_bf16x8(o + 8, g + 8);
+                        }
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kGMma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 2 * kGAccCols);
+    }
+}
+
+// ------------------------------------------------------------------ LoRA operands
+
+struct OperandParams {
+    const float* v;  // `parts` planes of [2][M][r_max], summed in plane order
+    int parts;
+    long long plane;
+    const int32_t* tok_adapter;
+    const int32_t* ranks;
+    const float* scales;
+    int M, n_adapters, r_max, r16;
+    uint16_t* ops;
+    int32_t* lists;
+    int32_t* list_len;
+};
+
+constexpr int kOpThreads = 128;
+constexpr int kOpParts = 8;  // CTAs per token tile, 16 rows each
+
+// s_a v of both slices as bf16 halves (columns past the rank zero), and per token tile the
+// adapters among its rows in order of first appearance.
+__global__ void __launch_bounds__(kOpThreads)
+operand_kernel(const OperandParams p)
+{
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kRows = kGTileM / kOpParts;
+    const int chunks = p.r16 >> 3, items = 2 * kRows * chunks;
+    for (int i = tid; i < items; i += kOpThreads) {
+        const int c = i % chunks, rs = i / chunks, s = rs / kRows;
+        const int row = m * kGTileM + (int)blockIdx.y * kRows + rs % kRows;
+        if (row >= p.M) continue;
+        const int a = p.tok_adapter[row];
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (a >= 0 && a < p.n_adapters) {
+            const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+            const float scale = p.scales ? p.scales[a] : 1.f;
+            if (8 * c < r) {
+                const float* src = p.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
+                for (int k = 0; k < p.parts; ++k) {
+                    const float4 x = *reinterpret_cast<const float4*>(src + k * p.plane);
+                    const float4 y = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
+                    f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+                    f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            lo[e] = pack_bf16x2(f[2 * e] - bf16_lo(hi[e]), f[2 * e + 1] - bf16_hi(hi[e]));
+        }
+        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
+        o[c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        o[chunks + c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (blockIdx.y != 0) return;
+    __shared__ int s_id[kGTileM];
+    __shared__ int s_cnt[kGTileM / 32];
+    const int row = m * kGTileM + tid;
+    int id = row < p.M ? p.tok_adapter[row] : -1;
+    if (id >= p.n_adapters) id = -1;
+    s_id[tid] = id;
+    __syncthreads();
+    bool first = id >= 0;
+    for (int j = 0; j < tid; ++j) first = first && s_id[j] != id;
+    const uint32_t mask = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) s_cnt[warp] = __popc(mask);
+    __syncthreads();
+    int at = __popc(mask & ((1u << lane) - 1u)), total = 0;
+    for (int w = 0; w < kGTileM / 32; ++w) {
+        if (w < warp) at += s_cnt[w];
+        total += s_cnt[w];
+    }
+    if (first) p.lists[m * kGTileM + at] = id;
+    if (tid == 0) p.list_len[m] = total;
+}
+
+// The columns of a tile: the smallest of rounds x columns (rounds of the grid over the SMs), where
+// narrow tiles pay for reading their operands from shared memory more often per product
+// once the products bound the call (more than one token tile).
+int tile_cols(int NC, int mt, int sms, const int* choices, int n_choices, const float* cost)
+{
+    int best = choices[0];
+    double least = 0;
+    for (int i = 0; i < n_choices; ++i) {
+        const long long tiles = (long long)mt * ((NC + choices[i] - 1) / choices[i]);
+        const double v = (double)((tiles + sms - 1) / sms) * choices[i] * (mt > 1 ? cost[i] : 1.f);
+        if (i == 0 || v < least) {
+            least = v;
+            best = choices[i];
+        }
+    }
+    return best;
+}
+
+template <int MODE, bool LORA>
+cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int grid, cudaStream_t stream)
+{
+    auto kern = gated_gemm_kernel<MODE, LORA>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kGThreads, 1, 1);
+    cfg.dynamicSmemBytes = kGSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+}
+
+}  // namespace
+
+size_t gated_operand_bytes(int M, int r_max)
+{
+    const size_t r16 = (size_t)(r_max + 15) / 16 * 16;
+    return (size_t)2 * M * 2 * r16 * 2;
+}
+size_t gated_list_bytes(int M)
+{
+    const size_t mt = (size_t)(M + kGTileM - 1) / kGTileM;
+    return mt * (kGTileM + 1) * 4;
+}
+
+cudaError_t launch_gated_operands(const float* v, int parts, const lora_pool_t& pool, const lora_segments_t& seg, int M,
+                                  void* ops, void* lists, cudaStream_t stream)
+{
+    const int mt = (M + kGTileM - 1) / kGTileM;
+    OperandParams p = {};
+    p.v = v;
+    p.parts = parts;
+    p.plane = (long long)pool.n_slices * M * pool.r_max;
+    p.tok_adapter = seg.tok_adapter;
+    p.ranks = pool.ranks;
+    p.scales = pool.scales;
+    p.M = M;
+    p.n_adapters = pool.n_adapters;
+    p.r_max = pool.r_max;
+    p.r16 = (pool.r_max + 15) / 16 * 16;
+    p.ops = static_cast<uint16_t*>(ops);
+    p.lists = static_cast<int32_t*>(lists);
+    p.list_len = p.lists + (size_t)mt * kGTileM;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)mt, kOpParts, 1);
+    cfg.blockDim = dim3(kOpThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, operand_kernel, p);
+}
+
+cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
+{
+    const bool bwd = a.backward;
+    GatedParams p = {};
+    p.M = a.M;
+    p.NC = bwd ? a.K : a.F;
+    p.mt = (a.M + kGTileM - 1) / kGTileM;
+    const int sms = device_sm_count();
+    const bool save = a.g8 != nullptr;
+    if (bwd) {
+        static const int c[] = {256, 192, 128, 64};
+        static const float cost[] = {1.f, 1.04f, 1.15f, 1.8f};
+        p.cols = tile_cols(p.NC, p.mt, sms, c, 4, cost);
+        p.bn = p.cols;
+    } else {
+        static const int c[] = {128, 96, 64, 32, 112, 80, 48, 16};  // checkpoint blocks: multiples of 32
+        static const float cost[] = {1.f, 1.04f, 1.15f, 1.8f, 1.02f, 1.08f, 1.4f, 3.f};
+        p.cols = tile_cols(p.NC, p.mt, sms, c, save ? 4 : 8, cost);
+        p.bn = 2 * p.cols;
+    }
+    p.tiles = p.mt * ((p.NC + p.cols - 1) / p.cols);
+    const int red = bwd ? a.F : a.K;
+    p.kb_half = (red + kGKBlock - 1) / kGKBlock;
+    p.kb = bwd ? 2 * p.kb_half : p.kb_half;
+    // few tokens: only their rows (in eights) are loaded; the MMA's other rows read whatever
+    // the shared memory holds and land in accumulator rows that nobody drains
+    const int a_rows = a.M >= kGTileM ? kGTileM : (a.M + 7) / 8 * 8;
+    p.a_bytes = a_rows * 128;
+    p.stage_bytes = p.a_bytes + p.bn * 128;
+    if (a.lora) {
+        p.r16 = (a.r_max + 15) / 16 * 16;
+        const int need = (bwd ? 1 : 2) * p.a_bytes + (p.cols + 63) / 64 * p.r16 * 128;
+        if (need > p.stage_bytes) p.stage_bytes = (need + 1023) / 1024 * 1024;
+    }
+    // 16 KB behind the last stage: what the MMA may read past a short A tile
+    const int room = kGSmem - kGBarBytes - 1024 - (a_rows < kGTileM ? kGTileM * 128 : 0);
+    p.stages = room / p.stage_bytes;
+    if (p.stages > kGMaxStages) p.stages = kGMaxStages;
+    p.act = a.act;
+    p.out = static_cast<uint16_t*>(a.out);
+    if (save) {
+        p.g_codes = a.g8->codes;
+        p.g_scales = a.g8->scales;
+        p.u_codes = a.u8->codes;
+        p.u_scales = a.u8->scales;
+    }
+    p.status = a.status;
+    p.timeout_ns = debug_wait_limit_ns();
+    p.inject_stall = debug_inject_stall();
+    if (a.lora) {
+        p.ops = static_cast<const uint16_t*>(a.ops);
+        p.B = static_cast<const uint16_t*>(a.B);
+        p.lists = static_cast<const int32_t*>(a.lists);
+        p.list_len = p.lists + (size_t)p.mt * kGTileM;
+        p.tok_adapter = a.tok_adapter;
+        p.ranks = a.ranks;
+        p.n_adapters = a.n_adapters;
+        p.r_max = a.r_max;
+    }
+    CUtensorMap tm[4];
+    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    bool ok = true;
+    for (int i = 0; i < 2; ++i) {
+        ok = ok && encode_tmap_2d(&tm[i], dt, bwd ? a.a[i] : a.a[0], (uint64_t)red, (uint64_t)a.M, (uint64_t)red * 2,
+                                  kGKBlock, (uint32_t)a_rows, sw);
+        ok = ok && encode_tmap_2d(&tm[2 + i], dt, a.W[i], (uint64_t)a.K, (uint64_t)a.F, (uint64_t)a.K * 2, kGKBlock,
+                                  bwd ? kGKBlock : (uint32_t)p.cols, sw);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const int grid = p.tiles < sms ? p.tiles : sms;
+    if (bwd)
+        return a.lora ? launch_mode<kGBwd, true>(tm, p, grid, stream) : launch_mode<kGBwd, false>(tm, p, grid, stream);
+    return a.lora ? launch_mode<kGFwd, true>(tm, p, grid, stream) : launch_mode<kGFwd, false>(tm, p, grid, stream);
+}
+
+}  // namespace lora

@@ -1,0 +1,333 @@
+// gated_grad.cu -- the gated feed-forward block's backward around its matrix product
+// (gated.cu): the element-wise part, read from the 8-bit checkpoints, and the adapters'
+// gradients.
+//
+//   dg = dh u act'(g),  du = dh act(g),  h = act(g) u          (g, u: act8.cuh)
+//   dA_s,a = x_a^T (s_a d_s B_s,a^T),  dB_s,a = (s_a x A_s,a)_a^T d_s
+//                                       (s = 0: gate, d = dg; s = 1: up, d = du)
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "act8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "sgmv_common.cuh"
+
+namespace lora {
+namespace {
+
+// ------------------------------------------------------------------ element-wise part
+//
+// Bound by HBM: per element 2 bytes of dh and 2 1/16 of checkpoints in, 4 bytes out (6 with
+// h). dg and du are rounded to bf16, as the product's operands have to be. A warp takes 256
+// columns of a row at a time, 8 per lane, two such tasks in flight.
+
+constexpr int kEThreads = 256;
+constexpr int kEWarps = kEThreads / 32;
+constexpr int kETaskCols = 256;
+constexpr int kEInFlight = 2;
+constexpr int kECtasPerSm = 6;
+
+struct PointParams {
+    const uint16_t* dh;
+    const uint8_t *g_codes, *g_scales, *u_codes, *u_scales;
+    uint16_t *dg, *du, *h;
+    int F;
+    uint32_t tasks, segs;
+};
+
+// act(g) and act'(g).
+template <int ACT>
+__device__ __forceinline__ void act_and_slope(float g, float& a, float& d)
+{
+    if (ACT == LORA_ACT_SILU) {
+        const float s = __fdividef(1.f, 1.f + __expf(-g));
+        a = g * s;
+        d = s * fmaf(g, 1.f - s, 1.f);
+    } else {
+        const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+        a = g * cdf;
+        d = fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), cdf);
+    }
+}
+
+template <int ACT, bool H>
+__global__ void __launch_bounds__(kEThreads)
+gated_point_kernel(const PointParams p)
+{
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const uint32_t stride = gridDim.x * kEWarps, nb = (uint32_t)((p.F + act8::kBlock - 1) / act8::kBlock);
+    for (uint64_t t0 = blockIdx.x * kEWarps + (threadIdx.x >> 5); t0 < p.tasks; t0 += (uint64_t)stride * kEInFlight) {
+        uint4 dh[kEInFlight];
+        uint2 gc[kEInFlight], uc[kEInFlight];
+        uint32_t gE[kEInFlight], uE[kEInFlight];
+        size_t at[kEInFlight];
+        bool live[kEInFlight];
+#pragma unroll
+        for (int i = 0; i < kEInFlight; ++i) {
+            const uint64_t t = t0 + (uint64_t)i * stride;
+            live[i] = false;
+            if (t < p.tasks) {
+                const uint32_t row = (uint32_t)t / p.segs;
+                const int col = (int)((uint32_t)t - row * p.segs) * kETaskCols + lane * 8;
+                if (col < p.F) {
+                    live[i] = true;
+                    at[i] = (size_t)row * p.F + col;
+                    const size_t sc = (size_t)row * nb + (col >> 5);
+                    dh[i] = __ldcs(reinterpret_cast<const uint4*>(p.dh + at[i]));
+                    gc[i] = __ldcs(reinterpret_cast<const uint2*>(p.g_codes + at[i]));
+                    uc[i] = __ldcs(reinterpret_cast<const uint2*>(p.u_codes + at[i]));
+                    gE[i] = p.g_scales[sc];
+                    uE[i] = p.u_scales[sc];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kEInFlight; ++i) {
+            if (!live[i]) continue;
+            const float gX = act8::scale_value(gE[i]), uX = act8::scale_value(uE[i]);
+            const uint32_t w[4] = {dh[i].x, dh[i].y, dh[i].z, dh[i].w};
+            uint32_t og[4], ou[4], oh[4];
+            float gv[8], uv[8];
+            act8::decode4(gc[i].x, gv);
+            act8::decode4(gc[i].y, gv + 4);
+            act8::decode4(uc[i].x, uv);
+            act8::decode4(uc[i].y, uv + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float a[2], d[2], u[2];
+                const float dy[2] = {bf16_lo(w[e]), bf16_hi(w[e])};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    act_and_slope<ACT>(gv[2 * e + k] * gX, a[k], d[k]);
+                    u[k] = uv[2 * e + k] * uX;
+                }
+                og[e] = pack_bf16x2(dy[0] * u[0] * d[0], dy[1] * u[1] * d[1]);
+                ou[e] = pack_bf16x2(dy[0] * a[0], dy[1] * a[1]);
+                oh[e] = pack_bf16x2(a[0] * u[0], a[1] * u[1]);
+            }
+            *reinterpret_cast<uint4*>(p.dg + at[i]) = make_uint4(og[0], og[1], og[2], og[3]);
+            *reinterpret_cast<uint4*>(p.du + at[i]) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            if (H) *reinterpret_cast<uint4*>(p.h + at[i]) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ adapters' gradients
+//
+// A segmented sum of outer products over an adapter's tokens: G[l][j] = sum_t lng[t][l] op[t][j],
+// lng = x (dA, l along K) or d_s (dB, l along F), op = the bf16 halves hi + lo of s_a u or s_a v
+// that operand_kernel wrote (about 16 bits). On mma.sync m16n8k16: the tensor work is
+// 2 r times the long elements, small beside reading them, so HBM bounds it. A CTA owns 64
+// values of l of one adapter and slice and walks the adapter's tokens 64 at a time, gathered
+// by cp.async into three stages; both operands come out of [token][value] rows by transposing
+// ldmatrix. Sums run in token order: the result does not depend on the grid. Adapters without
+// tokens get zeros.
+
+constexpr int kOThreads = 128;
+constexpr int kOTok = 64;
+constexpr int kOL = 64;
+constexpr int kOStages = 3;
+
+struct OuterParams {
+    const uint16_t* lng;
+    long long lng_slice;
+    const uint16_t* ops;  // [2][M][hi r16 | lo r16]
+    uint16_t* out;        // dA [2][n][L][r_max] or dB [2][n][r_max][L]
+    const int32_t* perm;
+    const int32_t* indptr;
+    const int32_t* ranks;
+    int M, L, n_adapters, r_max;
+};
+
+// Byte offset of 16-byte chunk c of row t, rows of CH chunks, laid out so that eight
+// consecutive rows' chunks c fall on different banks.
+template <int CH>
+__device__ __forceinline__ uint32_t o_chunk(int t, int c)
+{
+    if (CH == 4) return (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+    return (uint32_t)(t * CH * 16 + ((c ^ (t & 7)) << 4));
+}
+
+template <bool LONG_ROWS, int R16>
+__global__ void __launch_bounds__(kOThreads)
+gated_outer_kernel(const OuterParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kOpCh = R16 / 4;               // 16-byte chunks of an operand row (hi and lo)
+    constexpr int kLngBytes = kOTok * kOL * 2, kOpBytes = kOTok * kOpCh * 16, kStage = kLngBytes + kOpBytes;
+    constexpr int NT = R16 / 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int l0 = (int)blockIdx.x * kOL, a = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
+    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+    const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
+    const uint16_t* ops = p.ops + (size_t)s * p.M * (2 * R16);
+    const uint32_t base = ptx::smem_u32(smem);
+    const int steps = (n_tok + kOTok - 1) / kOTok;
+
+    auto fetch = [&](int step) {
+        if (step < steps) {
+            const uint32_t st = base + (uint32_t)((step % kOStages) * kStage);
+#pragma unroll
+            for (int i = 0; i < kOTok * (kOL / 8) / kOThreads; ++i) {
+                const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * kOTok + t;
+                const bool in = pos < n_tok && l0 + c * 8 < p.L;
+                const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * p.L + l0 + c * 8 : lng;
+                ptx::cp_async16(st + o_chunk<8>(t, c), src, in ? 16 : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kOTok * kOpCh / kOThreads; ++i) {
+                const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * kOTok + t;
+                const bool in = pos < n_tok;
+                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
+                ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
+            }
+        }
+        ptx::cp_async_commit();
+    };
+
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    for (int k = 0; k < kOStages - 1; ++k) fetch(k);
+    for (int step = 0; step < steps; ++step) {
+        ptx::cp_async_wait<kOStages - 2>();
+        __syncthreads();  // the step's rows are here, and the previous step's are consumed
+        fetch(step + kOStages - 1);
+        const uint32_t st = base + (uint32_t)((step % kOStages) * kStage), so = st + kLngBytes;
+        const int i = lane >> 3, rr = lane & 7;
+#pragma unroll
+        for (int ks = 0; ks < kOTok / 16; ++ks) {
+            uint32_t A[4];
+            ptx::ldsm_x4_t(st + o_chunk<8>(ks * 16 + (i >> 1) * 8 + rr, warp * 2 + (i & 1)), A[0], A[1], A[2], A[3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t b[4];
+                    ptx::ldsm_x4_t(so + o_chunk<kOpCh>(ks * 16 + (i & 1) * 8 + rr, h * NT + n + (i >> 1)), b[0], b[1], b[2],
+                                   b[3]);
+                    ptx::mma_bf16_16816(acc[n], A, b[0], b[1]);
+                    ptx::mma_bf16_16816(acc[n + 1], A, b[2], b[3]);
+                }
+        }
+    }
+    ptx::cp_async_wait<0>();
+    // one rounding to the adapters' type; columns past the rank are zero
+    const int g = lane >> 2, q = lane & 3;
+    if (LONG_ROWS) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int j = n * 8 + q * 2;
+            if (j >= p.r_max) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int l = l0 + warp * 16 + g + h * 8;
+                if (l < p.L)
+                    *reinterpret_cast<uint32_t*>(p.out + (((size_t)s * p.n_adapters + a) * p.L + l) * p.r_max + j) =
+                        pack_bf16x2(j < r ? acc[n][2 * h] : 0.f, j + 1 < r ? acc[n][2 * h + 1] : 0.f);
+            }
+        }
+    } else {
+        __syncthreads();
+        uint16_t* o = reinterpret_cast<uint16_t*>(smem);  // [R16][64], 8 elements of padding per row
+        constexpr int kPitch = kOL + 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = n * 8 + q * 2 + (e & 1), l = warp * 16 + g + (e >> 1) * 8;
+                o[j * kPitch + l] = (uint16_t)(pack_bf16x2(j < r ? acc[n][e] : 0.f, 0.f) & 0xffffu);
+            }
+        __syncthreads();
+        for (int idx = tid; idx < p.r_max * (kOL / 8); idx += kOThreads) {
+            const int j = idx >> 3, c = idx & 7, l = l0 + c * 8;
+            if (l < p.L)
+                *reinterpret_cast<uint4*>(p.out + (((size_t)s * p.n_adapters + a) * p.r_max + j) * p.L + l) =
+                    *reinterpret_cast<const uint4*>(o + j * kPitch + c * 8);
+        }
+    }
+}
+
+template <bool LONG_ROWS, int R16>
+cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
+{
+    const size_t smem = (size_t)kOStages * (kOTok * kOL * 2 + kOTok * R16 * 4);
+    auto kern = gated_outer_kernel<LONG_ROWS, R16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.L + kOL - 1) / kOL), (unsigned)p.n_adapters, 2);
+    cfg.blockDim = dim3(kOThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
+                               void* dg, void* du, void* h, cudaStream_t stream)
+{
+    PointParams p = {};
+    p.dh = static_cast<const uint16_t*>(dh);
+    p.g_codes = g8.codes;
+    p.g_scales = g8.scales;
+    p.u_codes = u8.codes;
+    p.u_scales = u8.scales;
+    p.dg = static_cast<uint16_t*>(dg);
+    p.du = static_cast<uint16_t*>(du);
+    p.h = static_cast<uint16_t*>(h);
+    p.F = F;
+    p.segs = (uint32_t)((F + kETaskCols - 1) / kETaskCols);
+    p.tasks = (uint32_t)M * p.segs;
+    const uint32_t most = (uint32_t)device_sm_count() * kECtasPerSm, need = (p.tasks + kEWarps - 1) / kEWarps;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(need < most ? need : most, 1, 1);
+    cfg.blockDim = dim3(kEThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (act == LORA_ACT_SILU)
+        return h ? cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_SILU, true>, p)
+                 : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_SILU, false>, p);
+    return h ? cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, true>, p)
+             : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, false>, p);
+}
+
+cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,
+                               const lora_pool_t& pool, const lora_segments_t& seg, void* out, cudaStream_t stream)
+{
+    OuterParams p = {};
+    p.lng = static_cast<const uint16_t*>(lng);
+    p.lng_slice = lng_slice;
+    p.ops = static_cast<const uint16_t*>(ops);
+    p.out = static_cast<uint16_t*>(out);
+    p.perm = seg.perm;
+    p.indptr = seg.indptr;
+    p.ranks = pool.ranks;
+    p.M = M;
+    p.L = L;
+    p.n_adapters = pool.n_adapters;
+    p.r_max = pool.r_max;
+    if (pool.r_max <= 16) return long_rows ? launch_outer<true, 16>(p, stream) : launch_outer<false, 16>(p, stream);
+    if (pool.r_max == 32) return long_rows ? launch_outer<true, 32>(p, stream) : launch_outer<false, 32>(p, stream);
+    return long_rows ? launch_outer<true, 64>(p, stream) : launch_outer<false, 64>(p, stream);
+}
+
+}  // namespace lora

@@ -66,6 +66,45 @@ cudaError_t launch_quantize_rows(const void* x, const int32_t* perm, int M, int 
 // E2M1 codes (element 2i in the low nibble), Wsc E8M0 [ceil(N / 128)][K / 32][128].
 cudaError_t launch_mxfp4_quantize(const void* W, int N, int K, uint8_t* Wp, uint8_t* Wsc, cudaStream_t stream);
 
+// 8-bit activation checkpoints (act8.cu): M rows of N bf16 compressed and expanded again.
+cudaError_t launch_act8_compress(const void* x, int M, int N, const lora_act8_t& out, cudaStream_t stream);
+cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cudaStream_t stream);
+
+// The gated feed-forward block. launch_gated_operands turns `parts` planes of v
+// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes) and lists the adapters
+// of each 128-token tile (gated_list_bytes); with adapters it is the launch right before
+// launch_gated_gemm (gated.cu says why).
+size_t gated_operand_bytes(int M, int r_max);
+size_t gated_list_bytes(int M);
+cudaError_t launch_gated_operands(const float* v, int parts, const lora_pool_t& pool, const lora_segments_t& seg, int M,
+                                  void* ops, void* lists, cudaStream_t stream);
+struct GatedGemmArgs {
+    bool backward;
+    int M, K, F, act;
+    const void* a[2];       // forward: x in a[0]; backward: dg, du [M][F]
+    const void* W[2];       // Wg, Wu [F][K]
+    void* out;              // h [M][F]; backward: dX [M][K]
+    const lora_act8_t* g8;  // forward: both or neither
+    const lora_act8_t* u8;
+    uint32_t* status;
+    bool lora;
+    const void* ops;
+    const void* lists;
+    const void* B;          // [2][n_adapters][r_max][F], backward: the transposed A [2][n_adapters][r_max][K]
+    const int32_t* tok_adapter;
+    const int32_t* ranks;
+    int n_adapters, r_max;
+};
+// cudaErrorInvalidValue if an operand's tensor map is refused.
+cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream);
+// dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu).
+cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
+                               void* dg, void* du, void* h, cudaStream_t stream);
+// Gradients of both slices: out[s][a][l][j] (long_rows) or [s][a][j][l] = the sum over the
+// adapter's tokens of lng[s][t][l] op[s][t][j], bf16; lng_slice 0: both slices read one lng.
+cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,
+                               const lora_pool_t& pool, const lora_segments_t& seg, void* out, cudaStream_t stream);
+
 struct Fp8GemmArgs {
     int M, N, K;
     int esz;             // operand element bytes: 1 = E4M3 (kind::f8f6f4), 2 = bf16 (kind::f16)

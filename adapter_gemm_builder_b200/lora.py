@@ -32,6 +32,11 @@ LORA_OP_BF16_GEMM = 4
 LORA_OP_FP8_BACKWARD = 5
 LORA_OP_MXFP4_GEMM = 6
 LORA_OP_W8A16_GEMM = 7
+LORA_OP_BF16_GATED = 8
+LORA_OP_BF16_GATED_BACKWARD = 9
+
+LORA_ACT_SILU = 0
+LORA_ACT_GELU = 1
 
 EXPORTED = [
     "lora_workspace_size", "lora_workspace_init", "lora_workspace_status", "lora_build_segments",
@@ -40,7 +45,8 @@ EXPORTED = [
     "lora_segments_status", "fp8_gemm_lora_epilogue_noalloc", "lora_noalloc_scratch_bytes",
     "lora_noalloc_status", "lora_debug_set_wait_limit", "bf16_gemm_lora_epilogue",
     "lora_switch_merge", "fp8_lora_backward", "mxfp4_quantize_rows", "mxfp4_gemm_lora_epilogue",
-    "w8a16_gemm_lora_epilogue",
+    "w8a16_gemm_lora_epilogue", "act8_compress_rows", "act8_expand_rows",
+    "bf16_gated_gemm_lora_epilogue", "bf16_gated_lora_backward",
 ]
 
 
@@ -66,6 +72,10 @@ class lora_segments_t(ctypes.Structure):
                 ("active", ctypes.c_void_p), ("tiles", ctypes.c_void_p),
                 ("tok_adapter", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("T", ctypes.c_int32), ("n_adapters", ctypes.c_int32)]
+
+
+class lora_act8_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +120,10 @@ def load(path: str = LIB_PATH):
             "mxfp4_quantize_rows": (I, [P, I, I, P, P, P]),
             "mxfp4_gemm_lora_epilogue": (I, [P, I, I, I, P, P, P, P, P, P, Z, P]),
             "w8a16_gemm_lora_epilogue": (I, [P, I, I, I, P, P, P, P, P, P, Z, P]),
+            "act8_compress_rows": (I, [P, I, I, P, P]),
+            "act8_expand_rows": (I, [P, I, I, P, P]),
+            "bf16_gated_gemm_lora_epilogue": (I, [P, I, I, I, P, P, I, P, P, P, P, P, P, Z, P]),
+            "bf16_gated_lora_backward": (I, [P, P, P, I, I, I, P, P, I, P, P, P, P, P, P, P, P, P, Z, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -335,6 +349,131 @@ def fp8_lora_backward(x: torch.Tensor, dY: torch.Tensor, WqT: torch.Tensor, swT:
     _check(load().fp8_lora_backward(_ptr(x), _ptr(dY), M, K, N, _ptr(WqT), _ptr(swT),
                                     ctypes.byref(pool.c), ctypes.byref(seg.c), _ptr(dX), _ptr(dA),
                                     _ptr(dB), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise LoraError(LORA_ERR_INVALID_ARG, what)
+
+
+def _rows(t, shape, what: str, device=None):
+    """A contiguous bf16 tensor of this shape on one CUDA device, as the library reads it."""
+    _need(t.is_cuda and t.dtype is torch.bfloat16 and tuple(t.shape) == tuple(shape) and t.is_contiguous()
+          and (device is None or t.device == device), f"{what}: contiguous bf16 {tuple(shape)} on one GPU")
+
+
+class Act8:
+    """Device buffers of an 8-bit checkpoint of a bf16 array [M, N] (see lora_act8_t): codes uint8
+    [M, N], scales uint8 [M, ceil(N / 32)]."""
+
+    def __init__(self, M: int, N: int, device="cuda"):
+        self._hold(torch.empty((M, N), dtype=torch.uint8, device=device),
+                   torch.empty((M, (N + 31) // 32), dtype=torch.uint8, device=device))
+
+    @classmethod
+    def of(cls, codes: torch.Tensor, scales: torch.Tensor) -> "Act8":
+        """A checkpoint over existing buffers."""
+        a = cls.__new__(cls)
+        a._hold(codes, scales)
+        return a
+
+    def _hold(self, codes, scales):
+        M, N = codes.shape
+        _need(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
+              and scales.is_contiguous() and tuple(scales.shape) == (M, (N + 31) // 32)
+              and codes.device == scales.device, "checkpoint: contiguous uint8 codes [M, N], scales [M, ceil(N / 32)]")
+        self.codes, self.scales = codes, scales
+        self.c = lora_act8_t(codes.data_ptr(), scales.data_ptr())
+
+    @property
+    def shape(self): return self.codes.shape
+
+
+def _act8(a: "Act8 | None", shape, what: str, device=None):
+    """Its C struct, or NULL."""
+    if a is None:
+        return None
+    _need(a.codes.is_cuda and tuple(a.shape) == tuple(shape) and (device is None or a.codes.device == device),
+          f"{what}: a checkpoint of {tuple(shape)} on one GPU")
+    return ctypes.byref(a.c)
+
+
+def _on(device, stream):
+    """The device made current for a launch, and the stream (the device's current one by default)."""
+    return torch.cuda.device(device), _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def act8_compress_rows(x: torch.Tensor, out: Act8, stream=None) -> None:
+    """out = the 8-bit checkpoint of x (bf16 [M, N], N % 16 == 0)."""
+    M, N = x.shape
+    _rows(x, (M, N), "x")
+    c = _act8(out, (M, N), "out", x.device)
+    guard, s = _on(x.device, stream)
+    with guard:
+        _check(load().act8_compress_rows(_ptr(x), M, N, c, s))
+
+
+def act8_expand_rows(a: Act8, x: torch.Tensor, stream=None) -> None:
+    """x = the bf16 values that the checkpoint stands for."""
+    M, N = a.shape
+    _rows(x, (M, N), "x")
+    c = _act8(a, (M, N), "a", x.device)
+    guard, s = _on(x.device, stream)
+    with guard:
+        _check(load().act8_expand_rows(c, M, N, _ptr(x), s))
+
+
+def bf16_gated_gemm_lora_epilogue(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, pool: Pool | None,
+                                  seg: Segments | None, h: torch.Tensor, ws: torch.Tensor, act: int = LORA_ACT_SILU,
+                                  save: "tuple[Act8, Act8] | None" = None, stream=None) -> None:
+    """h = act(g) * u with g = x.Wg^T + s_a (x.A[0]_a).B[0]_a and u = x.Wu^T + s_a (x.A[1]_a).B[1]_a
+    (Wg, Wu [F, K]; a pool of two slices). save: the checkpoints that g and u are also written to."""
+    M, K = x.shape
+    F = Wg.shape[0]
+    dev = x.device
+    _rows(x, (M, K), "x")
+    _rows(Wg, (F, K), "Wg", dev)
+    _rows(Wu, (F, K), "Wu", dev)
+    _rows(h, (M, F), "h", dev)
+    g8, u8 = (None, None) if save is None else (_act8(save[0], (M, F), "save[0]", dev), _act8(save[1], (M, F), "save[1]", dev))
+    guard, s = _on(dev, stream)
+    with guard:
+        _check(load().bf16_gated_gemm_lora_epilogue(
+            _ptr(x), M, K, F, _ptr(Wg), _ptr(Wu), act, ctypes.byref(pool.c) if pool else None,
+            ctypes.byref(seg.c) if seg else None, _ptr(h), g8, u8, _ptr(ws), ws.numel(), s))
+
+
+def bf16_gated_lora_backward(dh: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, pool: Pool | None,
+                             seg: Segments | None, g8: Act8, u8: Act8, x: "torch.Tensor | Act8 | None",
+                             dX: torch.Tensor, dA: torch.Tensor | None, dB: torch.Tensor | None, ws: torch.Tensor,
+                             act: int = LORA_ACT_SILU, h: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of the gated block on a frozen base from the checkpoints of g and u (see
+    bf16_gated_lora_backward): dX, with a pool dA [2, n, K, r_max] and dB [2, n, r_max, F], and
+    with h also act(g) * u. x (with a pool): bf16 or its checkpoint."""
+    M, F = dh.shape
+    K = Wg.shape[1]
+    dev = dh.device
+    _rows(dh, (M, F), "dh")
+    _rows(Wg, (F, K), "Wg", dev)
+    _rows(Wu, (F, K), "Wu", dev)
+    _rows(dX, (M, K), "dX", dev)
+    if h is not None:
+        _rows(h, (M, F), "h", dev)
+    _need(g8 is not None and u8 is not None, "g8, u8: checkpoints of g and u")
+    x8 = x if isinstance(x, Act8) else None
+    if pool is not None:
+        n, r = pool.c.n_adapters, pool.c.r_max
+        _need(x is not None and dA is not None and dB is not None, "x, dA and dB: required with a pool")
+        _rows(dA, (2, n, K, r), "dA", dev)
+        _rows(dB, (2, n, r, F), "dB", dev)
+        if x8 is None:
+            _rows(x, (M, K), "x", dev)
+    guard, s = _on(dev, stream)
+    with guard:
+        _check(load().bf16_gated_lora_backward(
+            None if x8 is not None else _ptr(x), _act8(x8, (M, K), "x", dev), _ptr(dh), M, K, F, _ptr(Wg), _ptr(Wu), act,
+            ctypes.byref(pool.c) if pool else None, ctypes.byref(seg.c) if seg else None, _act8(g8, (M, F), "g8", dev),
+            _act8(u8, (M, F), "u8", dev), _ptr(h), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), s))
 
 
 def lora_switch_merge(W: torch.Tensor, pool: Pool, sel: torch.Tensor, gates: torch.Tensor,

@@ -147,6 +147,8 @@ LORA_API int lora_segments_status(const lora_segments_t* seg, lora_stream_t stre
 #define LORA_OP_FP8_BACKWARD 5
 #define LORA_OP_MXFP4_GEMM 6
 #define LORA_OP_W8A16_GEMM 7
+#define LORA_OP_BF16_GATED 8
+#define LORA_OP_BF16_GATED_BACKWARD 9
 
 /*
  * Bytes of workspace an operation needs (0 if it needs none), or (size_t)-1
@@ -426,6 +428,83 @@ LORA_API int fp8_lora_backward(const void* x, const void* dY, int M, int K, int 
  */
 LORA_API int lora_switch_merge(const void* W, int N, int K, const lora_pool_t* pool, const int32_t* sel,
                                const float* gates, int n_sel, void* W_out, lora_stream_t stream);
+
+/*
+ * 8-bit activation checkpoint of a bf16 array [M][N] (device arrays, caller-owned): what a
+ * trainer keeps of an activation between its forward and its backward, 8.25 bits an element.
+ *   codes  e4m3 [M][N]
+ *   scales uint8 [M][ceil(N / 32)], E8M0: a block of 32 columns (the last of a row may be 16)
+ *          shares the scale X = 2^(scale - 127).
+ */
+typedef struct {
+    uint8_t* codes;
+    uint8_t* scales;
+} lora_act8_t;
+
+/*
+ * Compress bf16 rows. A block's X is the smallest power of two with amax <= 448 X, amax
+ * over its finite elements (at least 2^-127; scale 0 for an all-zero block), so nothing
+ * saturates; codes[m][n] = E4M3(x[m][n] / X), round to nearest even (the division is exact).
+ * An infinity or NaN is stored as NaN and does not touch its block's scale.
+ *   x bf16 [M][N]. N % 16 == 0; M may be 0. One kernel launch.
+ */
+LORA_API int act8_compress_rows(const void* x, int M, int N, const lora_act8_t* out, lora_stream_t stream);
+
+/*
+ * Expand a checkpoint: x[m][n] = bf16(E4M3(codes[m][n]) X). Exact unless the value is
+ * subnormal in bf16 (then rounded to nearest even). N % 16 == 0; M may be 0. One kernel launch.
+ */
+LORA_API int act8_expand_rows(const lora_act8_t* in, int M, int N, void* x, lora_stream_t stream);
+
+/* Activation of the gated feed-forward block. */
+#define LORA_ACT_SILU 0 /* z / (1 + exp(-z)) */
+#define LORA_ACT_GELU 1 /* z Phi(z), Phi the normal distribution (the erf form) */
+
+/*
+ * Gated feed-forward block of an adapted model, both projections, the adapters' term, the
+ * activation and the product in one GEMM (the MLP whose up projection the GEMM calls above
+ * compute alone; a = seg->tok_adapter[m], no term for -1 or pool == NULL):
+ *   g = x.Wg^T + s_a (x.A[0]_a).B[0]_a,   u = x.Wu^T + s_a (x.A[1]_a).B[1]_a   (fp32)
+ *   h = bf16(act(g) * u)
+ * g8 and u8 (both or neither): g and u are also written as 8-bit checkpoints, compressed from
+ * the fp32 sums (act8_compress_rows' rule), which is all bf16_gated_lora_backward needs of them.
+ *   x bf16 [M][K]; Wg, Wu bf16 [F][K]; h bf16 [M][F] (out).
+ *   pool: NULL, or n_slices == 2 (slice 0 the gate's adapters, slice 1 up's), h_in == K,
+ *   h_out == F. seg: required when pool != NULL (built for these M tokens).
+ *   ws: lora_workspace_size(LORA_OP_BF16_GATED, M, K, pool) bytes.
+ * With adapters: the shrink (v = x.A, fp32), a small kernel that lists each 128-token tile's
+ * adapters and puts s_a v into bf16 halves hi + lo, then the GEMM as its programmatic
+ * dependent; the term is part of the GEMM's sum. Its cost grows with the adapters per
+ * 128 consecutive tokens, so batches sorted by adapter cost least. Results do not depend on
+ * other tokens of the batch.
+ * Limits: M >= 1, K % 8 == 0, F % 8 == 0, F % 16 == 0 with checkpoints.
+ */
+LORA_API int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void* Wg, const void* Wu, int act,
+                                           const lora_pool_t* pool, const lora_segments_t* seg, void* h,
+                                           const lora_act8_t* g8, const lora_act8_t* u8, void* ws, size_t ws_bytes,
+                                           lora_stream_t stream);
+
+/*
+ * Backward of the gated block on a frozen base, from the 8-bit checkpoints of g and u:
+ *   dg = bf16(dh u act'(g)),  du = bf16(dh act(g))
+ *   dX = bf16(dg.Wg + du.Wu + s_a (dg.B[0]_a^T).A[0]_a^T + s_a (du.B[1]_a^T).A[1]_a^T)
+ *   dA[s]_a = bf16(s_a sum_m x_m (d_s,m.B[s]_a^T)),  dB[s]_a = bf16(s_a sum_m (x_m.A[s]_a) d_s,m)
+ * over the tokens m of adapter a (d_0 = dg, d_1 = du); columns of dA and rows of dB past an
+ * adapter's rank, and adapters without tokens, get zeros. Sums are fp32 in a fixed order.
+ *   dh bf16 [M][F]; Wg, Wu bf16 [F][K] as the forward has them; dX bf16 [M][K] (out).
+ *   h bf16 [M][F] (out) or NULL: act(g) u of the checkpointed g and u, the down projection's
+ *   input, for its own adapters' gradient.
+ *   With a pool (as for the forward): x bf16 [M][K] or x8, its checkpoint (exactly one of them;
+ *   x8 needs K % 16 == 0); dA bf16 [2][n_adapters][K][r_max], dB bf16 [2][n_adapters][r_max][F].
+ *   With pool == NULL, x, x8, dA and dB are not used (NULL).
+ *   ws: lora_workspace_size(LORA_OP_BF16_GATED_BACKWARD, M, F, pool) bytes (K there is the
+ *   backward's reduction size, F).
+ * Limits: M >= 1, K % 8 == 0, F % 16 == 0.
+ */
+LORA_API int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* dh, int M, int K, int F,
+                                      const void* Wg, const void* Wu, int act, const lora_pool_t* pool,
+                                      const lora_segments_t* seg, const lora_act8_t* g8, const lora_act8_t* u8, void* h,
+                                      void* dX, void* dA, void* dB, void* ws, size_t ws_bytes, lora_stream_t stream);
 
 /*
  * fp8_gemm_lora_epilogue for callers that cannot allocate device memory
