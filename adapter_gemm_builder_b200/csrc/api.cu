@@ -114,21 +114,6 @@ size_t bwd_ws_layout(int M, const lora_pool_t* pool, size_t* off_at, size_t* off
     return off;
 }
 
-// Planes of v that the shrink of a batch writes: the tensor-core shrink's for long
-// segments, one otherwise.
-int shrink_planes(int T, const lora_pool_t& pool) { return sgmv_expand_tc_eligible(T, pool) ? sgmv_shrink_tc_parts(pool) : 1; }
-
-// The pool whose A and B are the transposes (h_in and h_out swapped), for the backward.
-lora_pool_t transposed(const lora_pool_t& pool, void* At, void* Bt)
-{
-    lora_pool_t t = pool;
-    t.A = At;
-    t.B = Bt;
-    t.h_in = pool.h_out;
-    t.h_out = pool.h_in;
-    return t;
-}
-
 // Gated forward workspace: status | planes of v | operands | adapter lists (adapters only).
 struct GatedWs {
     size_t v, ops, lists, size;
@@ -139,7 +124,7 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     w.size = 256;
     if (!pool) return w;
     w.v = w.size;
-    w.size += align256(apply_v_bytes(M, *pool, shrink_planes(M, *pool)));
+    w.size += align256(apply_v_bytes(M, *pool, gated_shrink_planes(M, pool->h_in, pool->n_adapters)));
     w.ops = w.size;
     w.size += align256(gated_operand_bytes(M, pool->r_max));
     w.lists = w.size;
@@ -147,10 +132,10 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     return w;
 }
 
-// Gated backward workspace: status | dg, du | with adapters: x expanded | A' = B^T, B' = A^T of
-// both slices | planes of u, then of v | operands of u, of v | adapter lists.
+// Gated backward workspace: status | dg, du | with adapters: x expanded | planes of u, then of
+// v | operands of u, of v | adapter lists.
 struct GatedBwdWs {
-    size_t d, x, at, bt, v, ops_u, ops_v, lists, size;
+    size_t d, x, v, ops_u, ops_v, lists, size;
 };
 GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 {
@@ -159,17 +144,11 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
     w.d = w.size;
     w.size += align256((size_t)2 * M * F * 2);
     if (!pool) return w;
-    const size_t na = (size_t)pool->n_adapters;
     w.x = w.size;
     w.size += align256((size_t)M * pool->h_in * 2);
-    w.at = w.size;
-    w.size += align256(2 * na * F * pool->r_max * 2);
-    w.bt = w.size;
-    w.size += align256(2 * na * pool->r_max * pool->h_in * 2);
     w.v = w.size;
-    const lora_pool_t t = transposed(*pool, nullptr, nullptr);
-    const size_t a = apply_v_bytes(M, *pool, shrink_planes(M, *pool)), b = apply_v_bytes(M, t, shrink_planes(M, t));
-    w.size += align256(a > b ? a : b);
+    const int a = gated_shrink_planes(M, F, pool->n_adapters), b = gated_shrink_planes(M, pool->h_in, pool->n_adapters);
+    w.size += align256(apply_v_bytes(M, *pool, a > b ? a : b));
     w.ops_u = w.size;
     w.size += align256(gated_operand_bytes(M, pool->r_max));
     w.ops_v = w.size;
@@ -179,16 +158,20 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
     return w;
 }
 
-// v = x.A of both slices into planes at v, then its operands and the tiles' adapter lists.
-cudaError_t gated_operands(const void* x, int64_t x_slice_stride, const lora_pool_t& pool, const lora_segments_t& seg,
-                           int M, float* v, void* ops, void* lists, cudaStream_t s)
+// v = x.A (down) or d.B^T of both slices into planes at v, then its operands and the token tiles'
+// rank blocks. Decode-like batches (tiles of four tokens) of the forward take the cluster kernel,
+// which spreads a token's row over a cluster.
+cudaError_t gated_operands(bool down, const void* lng, int64_t lng_slice, const lora_pool_t& pool,
+                           const lora_segments_t& seg, int M, float* v, void* ops, void* lists, cudaStream_t s)
 {
-    int planes = shrink_planes(M, pool);
-    cudaError_t e = cudaErrorInvalidValue;
-    if (planes > 1 || sgmv_expand_tc_eligible(M, pool)) e = launch_sgmv_shrink_tc(x, x_slice_stride, pool, seg, v, planes, s);
-    if (e == cudaErrorInvalidValue) {  // short segments, or the pool's tensor map was refused
+    const int L = down ? pool.h_in : pool.h_out;
+    int planes = gated_shrink_planes(M, L, pool.n_adapters);
+    cudaError_t e;
+    if (down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
         planes = 1;
-        e = launch_sgmv(SGMV_SHRINK, x, x_slice_stride, pool, seg, v, nullptr, s, false);
+        e = launch_sgmv(SGMV_SHRINK, lng, lng_slice, pool, seg, v, nullptr, s, false);
+    } else {
+        e = launch_gated_shrink(down, lng, lng_slice, L, M, pool, seg, v, planes, s);
     }
     if (e != cudaSuccess) return e;
     return launch_gated_operands(v, planes, pool, seg, M, ops, lists, s);
@@ -682,7 +665,7 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
-        if (gated_operands(x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
+        if (gated_operands(true, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
             return LORA_ERR_CUDA;
         a.lora = true;
         a.ops = w + l.ops;
@@ -732,24 +715,15 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.out = dX;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (!pool) return cuda_status(launch_gated_gemm(a, s));
-    // 2. the transposed pools of the active adapters (A' = B^T, B' = A^T) and u = d.A'
-    const size_t na = (size_t)pool->n_adapters, at = na * F * pool->r_max, bt = na * pool->r_max * K;
-    lora_pool_t pt = transposed(*pool, w + l.at, w + l.bt);
+    // 2. u = d.B^T of both slices
     float* v = reinterpret_cast<float*>(w + l.v);
-    for (int i = 0; i < 2; ++i) {
-        lora_pool_t one = *pool;
-        one.A = static_cast<const uint16_t*>(pool->A) + i * bt;
-        one.B = static_cast<const uint16_t*>(pool->B) + i * at;
-        if (launch_transpose_pool(one, *seg, reinterpret_cast<uint16_t*>(w + l.at) + i * at,
-                                  reinterpret_cast<uint16_t*>(w + l.bt) + i * bt, s) != cudaSuccess)
-            return LORA_ERR_CUDA;
-    }
-    if (gated_operands(dg, (int64_t)M * F, pt, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+    if (gated_operands(false, dg, (int64_t)M * F, *pool, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess)
+        return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
     a.ops = w + l.ops_u;
     a.lists = w + l.lists;
-    a.B = pt.B;
+    a.B = pool->A;
     a.tok_adapter = seg->tok_adapter;
     a.ranks = pool->ranks;
     a.n_adapters = pool->n_adapters;
@@ -760,7 +734,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
         if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
         x = w + l.x;
     }
-    if (gated_operands(x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
+    if (gated_operands(true, x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
         launch_gated_outer(true, x, 0, K, w + l.ops_u, M, *pool, *seg, dA, s) != cudaSuccess ||
         launch_gated_outer(false, dg, (int64_t)M * F, F, w + l.ops_v, M, *pool, *seg, dB, s) != cudaSuccess)
         return LORA_ERR_CUDA;

@@ -12,16 +12,22 @@
 // (one checkpoint scale) lies in one thread. Backward: the sum runs over dg then du (2F long),
 // and Wg, Wu [F][K] are read as they are, as the MMA's MN-major operand (no transposed copy).
 //
-// The LoRA term extends the sum of a tile: for every adapter that has tokens among the tile's
-// 128 rows (listed by operand_kernel below, in order of first appearance) one more ring stage per
-// slice holds v (the rows of other adapters zero) against B_a's rows. v comes as bf16 halves
-// hi + lo in the forward (about 16 bits of v: a checkpoint's codes must not flip by the
-// rounding of v) and as hi alone in the backward, whose dg and du are bf16 already. Tokens
-// stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens are sorted
-// by adapter has few adapters per tile.
+// The LoRA term extends the sum of a tile. operand_kernel below lists, for every 128 tokens, the
+// rank blocks (16 ranks of an adapter) that any of them uses; `ups` blocks fill one more ring
+// stage per slice: s_a v of the tile's rows (zero in the blocks of other adapters) against the
+// blocks of B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is
+// stored). v is split into bf16 parts that add up in the accumulator: hi + lo (16 bits of v), and
+// a third part where checkpoints are written, so that no code flips by the rounding of v
+// (two parts flipped codes three times as often as the fp32 sums do). Those stages lie between the main
+// ones in the second half of a tile's sum: the builders have the next stage's data in
+// registers before its slot is free, so a stage costs the ring a shared-memory write, not a
+// trip to memory (one stage per adapter at the end of the tile, loaded when its slot was free,
+// had cost about 2 us each: 160 us for 36 tokens of 32 adapters, 37 us without adapters).
+// Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
+// are sorted by adapter has few adapters per tile.
 //
-// Roles (448 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
-// chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..13 build
+// Roles (576 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
+// chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..17 build
 // the LoRA stages. Two accumulators (512 TMEM columns), so a tile drains under the next one's
 // products. Every wait is bounded; on expiry the CTA records a status word, lets what it
 // issued land and leaves.
@@ -39,7 +45,8 @@ namespace {
 
 constexpr int kGDrainWarps = 8;
 constexpr int kGProducer = kGDrainWarps, kGMma = kGProducer + 1, kGBuilder0 = kGMma + 1;
-constexpr int kGBuilders = 128;
+constexpr int kGBuilders = 256;
+constexpr int kGMaxA = 8, kGMaxB = 4;        // 16-byte pieces of a LoRA stage per builder
 constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
 constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 8;
@@ -47,6 +54,8 @@ constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16,
 constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
 constexpr int kGBarBytes = 512;
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
+constexpr int kOpParts = 3;                   // bf16 parts of v that operand_kernel writes
+constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);
 enum { kGFwd = 0, kGBwd = 1 };
 // status bits of the bounded waits
 enum { kGStRing = 0x1, kGStMma = 0x2, kGStBuild = 0x4, kGStDrain = 0x8, kGStStall = 0x10 };
@@ -64,10 +73,11 @@ struct GatedParams {
     unsigned long long timeout_ns;
     int inject_stall;
     // LoRA
-    const uint16_t* ops;      // [2][M][hi r16 | lo r16]: s_a v as bf16 halves
-    const uint16_t* B;        // [2][n_adapters][r_max][NC]
-    const int32_t* lists;     // [mt][128] adapters of a token tile
+    const uint16_t* ops;      // [2][M][kOpParts][r16]: s_a v in bf16 parts
+    const uint16_t* B;        // forward B [2][n_adapters][r_max][NC], backward A [2][n_adapters][NC][r_max]
+    const int32_t* lists;     // [mt][kListMax] rank blocks of a token tile: adapter * 4 + block
     const int32_t* list_len;  // [mt]
+    int parts, ups;           // parts of v used, rank blocks per stage
     const int32_t* tok_adapter;
     const int32_t* ranks;
     int n_adapters, r_max, r16;
@@ -129,6 +139,14 @@ __device__ __forceinline__ void save_block(const float* v, int n, uint8_t* codes
     *scale = (uint8_t)E;
 }
 
+// LoRA stages of token tile m: `ups` rank blocks each, both slices.
+__device__ __forceinline__ int lora_stages(const GatedParams& p, int m) { return 2 * ((p.list_len[m] + p.ups - 1) / p.ups); }
+// Where a LoRA stage's B part begins: behind the operand's tiles of 64 columns.
+__host__ __device__ __forceinline__ uint32_t lora_b_offset(const GatedParams& p)
+{
+    return (uint32_t)((p.parts * p.ups + 3) / 4 * p.a_bytes);
+}
+
 template <int MODE, bool LORA>
 __global__ void __launch_bounds__(kGThreads, 1)
 gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
@@ -171,8 +189,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         ptx::tmem_relinquish();
     }
     // Without adapters the operands may come from the kernel before this one. With them that
-    // kernel is operand_kernel, which let this one start only after all that ran before it was
-    // complete: x, dg, du and the weights may be read at once, its own outputs after the wait.
+    // kernel is operand_kernel, and the one before it the shrink, which let operand_kernel (and so
+    // this one) start only after all that ran before the shrink was complete: x, dg, du and the
+    // weights may be read at once, operand_kernel's outputs after the wait.
     if (!LORA) ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     ptx::tc_fence_before();
@@ -199,10 +218,12 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     ++use;
                 }
             };
-            bool waited = !LORA;
+            bool waited = false;
+            const int first = p.kb / 2;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
                 const int m = t % p.mt, n0 = (t / p.mt) * p.cols;
-                for (int kb = 0; kb < p.kb; ++kb) {
+                int ext = 0, acc = 0;  // LoRA stages of the tile, spread over its second half
+                for (int kb = 0; kb < p.kb && ok; ++kb) {
                     if (!(ok = acquire())) break;
                     const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
                     ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(p.a_bytes + p.bn * 128));
@@ -219,15 +240,18 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             ptx::tma_load_2d(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, &full[st], n0 + b * 64, f0);
                     }
                     next();
-                }
-                if (LORA && ok) {
-                    if (!waited) ptx::pdl_wait();
-                    waited = true;
-                    for (int e = 2 * p.list_len[m]; e > 0; --e) {
-                        if (!(ok = acquire())) break;
-                        last[st] = -1;
-                        ptx::mbar_arrive(&go[st]);
-                        next();
+                    if (LORA && kb >= first) {
+                        if (kb == first) {
+                            if (!waited) ptx::pdl_wait();
+                            waited = true;
+                            ext = lora_stages(p, m);
+                        }
+                        for (acc += ext; acc >= p.kb - first; acc -= p.kb - first) {
+                            if (!(ok = acquire())) break;
+                            last[st] = -1;
+                            ptx::mbar_arrive(&go[st]);
+                            next();
+                        }
                     }
                 }
             }
@@ -241,14 +265,16 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         if (lane == 0) {
             int st = 0, acc = 0;
             uint32_t use = 0;
-            bool ok = true, waited = !LORA;
+            bool ok = true, waited = false;
+            const int first = p.kb / 2;
             auto next = [&]() {
                 if (++st == p.stages) {
                     st = 0;
                     ++use;
                 }
             };
-            const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, true);
+            const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, MODE == kGFwd);
+            const uint32_t lora_b = lora_b_offset(p);
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++acc) {
                 const int m = t % p.mt, buf = acc & 1;
                 if (acc >= 2 &&
@@ -256,7 +282,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                                            p.timeout_ns)))
                     break;
                 const uint32_t d = tmem + (uint32_t)(buf * kGAccCols);
-                for (int kb = 0; kb < p.kb; ++kb) {
+                int ext = 0, acc_e = 0, e = 0, blocks = 0;
+                for (int kb = 0; kb < p.kb && ok; ++kb) {
                     if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
                     ptx::tc_fence_after();
                     const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
@@ -268,24 +295,30 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                                         id_main, (kb | ks) ? 1u : 0u);
                     ptx::tc_commit(&empty[st]);
                     next();
-                }
-                if (LORA && ok) {
-                    if (!waited) ptx::pdl_wait();
-                    waited = true;
-                    const int ext = 2 * p.list_len[m];
-                    for (int e = 0; e < ext; ++e) {
-                        if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
-                        ptx::tc_fence_after();
-                        const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes);
-                        const int halves = MODE == kGFwd ? 2 : 1;
-                        const uint32_t sb = sa + (uint32_t)(halves * p.a_bytes);
-                        const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
-                        for (int h = 0; h < halves; ++h)
-                            for (int ks = 0; ks < (p.r16 >> 4); ++ks)
-                                ptx::tc_mma_f16(ds, g_desc_k(sa + (uint32_t)(h * p.a_bytes + ks * 32)),
-                                                g_desc_mn(sb + (uint32_t)(ks * 2048), (uint32_t)(p.r16 * 128)), id_lora, 1u);
-                        ptx::tc_commit(&empty[st]);
-                        next();
+                    if (LORA && kb >= first) {
+                        if (kb == first) {
+                            if (!waited) ptx::pdl_wait();
+                            waited = true;
+                            blocks = p.list_len[m];
+                            ext = lora_stages(p, m);
+                        }
+                        for (acc_e += ext; acc_e >= p.kb - first; acc_e -= p.kb - first, ++e) {
+                            if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+                            ptx::tc_fence_after();
+                            const uint32_t la = base_u + (uint32_t)(st * p.stage_bytes), lb = la + lora_b;
+                            const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
+                            const int n = min(p.ups, blocks - (e >> 1) * p.ups);
+                            for (int part = 0; part < p.parts; ++part)
+                                for (int k = 0; k < n; ++k) {
+                                    const int c = part * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
+                                    ptx::tc_mma_f16(ds, g_desc_k(la + (uint32_t)((c >> 2) * p.a_bytes + (c & 3) * 32)),
+                                                    MODE == kGFwd ? g_desc_mn(lb + (uint32_t)(k * 2048), (uint32_t)(p.ups * 2048))
+                                                                  : g_desc_k(lb + (uint32_t)(k * 32)),
+                                                    id_lora, 1u);
+                                }
+                            ptx::tc_commit(&empty[st]);
+                            next();
+                        }
                     }
                 }
                 if (ok) ptx::tc_commit(&tfull[buf]);
@@ -299,51 +332,118 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         if (LORA) {
             ptx::pdl_wait();
             const int bt = threadIdx.x - kGBuilder0 * 32;
-            const int chunks = p.r16 >> 3, bpr = p.cols >> 3;  // 16-byte chunks of an operand row, of a B row
-            const int halves = MODE == kGFwd ? 2 : 1;
-            int st = 0;
-            uint32_t gos[kGMaxStages];  // fills of stage s so far
-            for (int s = 0; s < kGMaxStages; ++s) gos[s] = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-                const int m = t % p.mt, n0 = (t / p.mt) * p.cols, row = m * kGTileM + bt;
-                const int mine = row < p.M ? p.tok_adapter[row] : -1;
-                const int len = p.list_len[m];
-                st = (st + p.kb) % p.stages;
-                for (int e = 0; e < 2 * len && ok; ++e) {
-                    const int a = p.lists[m * kGTileM + (e >> 1)], s = e & 1;
-                    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
-                    uint32_t par = 0;
-#pragma unroll
-                    for (int i = 0; i < kGMaxStages; ++i)
-                        if (i == st) par = gos[i]++ & 1;
-                    // all builders take part or none (a wait that ran out may show in one warp only)
-                    ok = wait_all<false>(&go[st], par, abort_flag, status, kGStBuild, p.timeout_ns);
-                    ok = !ptx::named_sync_or(1, kGBuilders, !ok);
-                    if (!ok) break;
-                    uint8_t* sa = ring + st * p.stage_bytes;
-                    // v: this thread's row, zero for tokens of other adapters
-                    if (bt * 128 < p.a_bytes) {
-                        const uint4* src = reinterpret_cast<const uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
-                        for (int h = 0; h < halves; ++h)
-                            for (int c = 0; c < chunks; ++c)
-                                *reinterpret_cast<uint4*>(sa + h * p.a_bytes + bt * 128 + ((c ^ (bt & 7)) << 4)) =
-                                    mine == a ? src[h * chunks + c] : make_uint4(0u, 0u, 0u, 0u);
+            const int first = p.kb / 2, spread = p.kb - first;
+            // A builder's pieces lie in one column of 16-byte pieces, a fixed number of rows apart
+            // (a multiple of eight, so their swizzle is the same): piece i of the operand in row
+            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c.
+            const int a_cpr = 2 * p.ups * p.parts, a_lg = a_cpr <= 8 ? 3 : (a_cpr <= 16 ? 4 : 5);
+            const int a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
+            const int a_rows = a_c < a_cpr ? p.a_bytes >> 7 : 0;
+            const int b_cpr = MODE == kGFwd ? p.cols >> 3 : 2 * p.ups, b_lg = MODE == kGFwd ? 4 : (p.ups == 4 ? 3 : 2);
+            const int b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
+            const int b_rows = b_c < b_cpr ? (MODE == kGFwd ? 16 * p.ups : p.cols) : 0;
+            const int a_part = a_c / (2 * p.ups), a_k = a_c - a_part * 2 * p.ups;
+            const uint32_t a_off = (uint32_t)((a_c >> 3) * p.a_bytes + a_row * 128 + (((a_c & 7) ^ (a_row & 7)) << 4));
+            const uint32_t b_off = (uint32_t)((MODE == kGFwd ? (b_c >> 3) * (p.ups * 2048) : 0) + b_row * 128 +
+                                              (((b_c & 7) ^ (b_row & 7)) << 4));
+            const uint32_t lora_b = lora_b_offset(p);
+            // the walk over the ring: main stages are passed over, LoRA stages stopped at
+            int t = blockIdx.x, st = 0, k = 0, acc = 0, ext = 0, e = -1;
+            bool open = false, main_done = false;
+            int m = 0, n0 = 0;
+            auto advance = [&]() -> bool {  // to the next LoRA stage: (m, n0, e) in slot st
+                for (; t < p.tiles; t += gridDim.x, open = false) {
+                    if (!open) {
+                        m = t % p.mt;
+                        n0 = (t / p.mt) * p.cols;
+                        ext = lora_stages(p, m);
+                        st = (st + (ext ? first : p.kb)) % p.stages;
+                        k = ext ? 0 : spread;
+                        acc = 0;
+                        e = -1;
+                        open = true;
+                        main_done = false;
+                    } else if (e >= 0) {
+                        if (++st == p.stages) st = 0;  // past the LoRA stage stopped at
                     }
-                    // B_a's rows of these columns, zero past the rank and past the row's end
-                    uint8_t* sb = sa + halves * p.a_bytes;
-                    const uint16_t* Ba = p.B + ((size_t)s * p.n_adapters + a) * p.r_max * p.NC + n0;
-                    for (int i = bt; i < p.r16 * bpr; i += kGBuilders) {
-                        const int j = i / bpr, c = i - j * bpr;
-                        const bool in = j < r && n0 + c * 8 < p.NC;
-                        *reinterpret_cast<uint4*>(sb + (c >> 3) * (p.r16 * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
-                            in ? *reinterpret_cast<const uint4*>(Ba + (size_t)j * p.NC + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    for (; k < spread; ++k, main_done = false) {
+                        if (!main_done) {
+                            if (++st == p.stages) st = 0;
+                            acc += ext;
+                            main_done = true;
+                        }
+                        if (acc >= spread) {
+                            acc -= spread;
+                            ++e;
+                            return true;
+                        }
                     }
-                    ptx::fence_proxy_async_smem();
-                    ptx::named_sync(2, kGBuilders);
-                    if (bt == 0) ptx::mbar_arrive(&full[st]);
-                    if (++st == p.stages) st = 0;
                 }
+                return false;
+            };
+            uint4 ra[kGMaxA], rb[kGMaxB];
+            auto load = [&]() {  // the stage's pieces into registers; zero where nothing belongs
+                const int s = e & 1, b0 = (e >> 1) * p.ups;
+                const int32_t* list = p.lists + (size_t)m * kListMax;
+                const int blocks = p.list_len[m];
+                {
+                    const int u = b0 + (a_k >> 1) < blocks ? list[b0 + (a_k >> 1)] : -4;
+                    const size_t at = ((size_t)s * p.M * kOpParts + a_part) * p.r16 + (u & 3) * 16 + (a_k & 1) * 8;
+#pragma unroll
+                    for (int i = 0; i < kGMaxA; ++i) {
+                        const int row = a_row + i * a_step, tok = m * kGTileM + row;
+                        ra[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row < a_rows && tok < p.M && u >= 0 && p.tok_adapter[tok] == (u >> 2))
+                            ra[i] = *reinterpret_cast<const uint4*>(p.ops + at + (size_t)tok * (kOpParts * p.r16));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kGMaxB; ++i) {
+                    const int row = b_row + i * b_step, b = b0 + (MODE == kGFwd ? row >> 4 : b_c >> 1);
+                    rb[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row >= b_rows || b >= blocks) continue;
+                    const int u = list[b], a = u >> 2;
+                    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+                    const uint16_t* src = p.B + ((size_t)s * p.n_adapters + a) * p.r_max * p.NC;
+                    if (MODE == kGFwd) {  // row j of B_a, eight columns
+                        const int j = (u & 3) * 16 + (row & 15);
+                        if (j < r && n0 + b_c * 8 < p.NC)
+                            rb[i] = *reinterpret_cast<const uint4*>(src + (size_t)j * p.NC + n0 + b_c * 8);
+                    } else {  // row n of A_a, eight ranks; what lies past the rank is not read as a number
+                        const int j = (u & 3) * 16 + (b_c & 1) * 8, live = r - j;
+                        if (live > 0 && n0 + row < p.NC) {
+                            rb[i] = *reinterpret_cast<const uint4*>(src + (size_t)(n0 + row) * p.r_max + j);
+                            if (live < 8) {
+                                uint32_t* w = reinterpret_cast<uint32_t*>(&rb[i]);
+#pragma unroll
+                                for (int h = 0; h < 4; ++h)
+                                    w[h] &= live > 2 * h + 1 ? 0xffffffffu : (live > 2 * h ? 0xffffu : 0u);
+                            }
+                        }
+                    }
+                }
+            };
+            uint32_t gos = 0;  // bit s: parity of the next `go` of slot s
+            bool more = advance();
+            if (more) load();
+            while (more) {
+                // all builders take part or none (a wait that ran out may show in one warp only)
+                bool ok = wait_all<false>(&go[st], (gos >> st) & 1, abort_flag, status, kGStBuild, p.timeout_ns);
+                ok = !ptx::named_sync_or(1, kGBuilders, !ok);
+                if (!ok) break;
+                gos ^= 1u << st;
+                uint8_t *sa = ring + st * p.stage_bytes + a_off, *sb = ring + st * p.stage_bytes + lora_b + b_off;
+#pragma unroll
+                for (int i = 0; i < kGMaxA; ++i)
+                    if (a_row + i * a_step < a_rows) *reinterpret_cast<uint4*>(sa + i * a_step * 128) = ra[i];
+#pragma unroll
+                for (int i = 0; i < kGMaxB; ++i)
+                    if (b_row + i * b_step < b_rows) *reinterpret_cast<uint4*>(sb + i * b_step * 128) = rb[i];
+                ptx::fence_proxy_async_smem();
+                ptx::named_sync(2, kGBuilders);
+                if (bt == 0) ptx::mbar_arrive(&full[st]);
+                more = advance();
+                if (more) load();
             }
         }
     } else {
@@ -413,8 +513,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 // ------------------------------------------------------------------ LoRA operands
 
 struct OperandParams {
-    const float* v;  // `parts` planes of [2][M][r_max], summed in plane order
-    int parts;
+    const float* v;  // `planes` planes of [2][M][r_max], summed in plane order
+    int planes;
     long long plane;
     const int32_t* tok_adapter;
     const int32_t* ranks;
@@ -426,48 +526,51 @@ struct OperandParams {
 };
 
 constexpr int kOpThreads = 128;
-constexpr int kOpParts = 8;  // CTAs per token tile, 16 rows each
+constexpr int kOpCtas = 8;  // CTAs per token tile, 16 rows each
 
-// s_a v of both slices as bf16 halves (columns past the rank zero), and per token tile the
-// adapters among its rows in order of first appearance.
+// s_a v of both slices in kOpParts bf16 parts that add up to it (columns past the rank zero),
+// and per token tile the rank blocks that its rows use, adapters in order of first appearance.
+// Lets the GEMM start at once (see the wait there).
 __global__ void __launch_bounds__(kOpThreads)
 operand_kernel(const OperandParams p)
 {
-    ptx::pdl_wait();
     ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
     const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kRows = kGTileM / kOpParts;
+    constexpr int kRows = kGTileM / kOpCtas;
     const int chunks = p.r16 >> 3, items = 2 * kRows * chunks;
     for (int i = tid; i < items; i += kOpThreads) {
         const int c = i % chunks, rs = i / chunks, s = rs / kRows;
         const int row = m * kGTileM + (int)blockIdx.y * kRows + rs % kRows;
         if (row >= p.M) continue;
         const int a = p.tok_adapter[row];
+        if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
+        const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+        const float scale = p.scales ? p.scales[a] : 1.f;
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (a >= 0 && a < p.n_adapters) {
-            const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
-            const float scale = p.scales ? p.scales[a] : 1.f;
-            if (8 * c < r) {
-                const float* src = p.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
-                for (int k = 0; k < p.parts; ++k) {
-                    const float4 x = *reinterpret_cast<const float4*>(src + k * p.plane);
-                    const float4 y = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
-                    f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-                    f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-                }
+        if (8 * c < r) {
+            const float* src = p.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
+            for (int k = 0; k < p.planes; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(src + k * p.plane);
+                const float4 y = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
+                f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+                f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
         }
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-            lo[e] = pack_bf16x2(f[2 * e] - bf16_lo(hi[e]), f[2 * e + 1] - bf16_hi(hi[e]));
+        for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
+        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (kOpParts * p.r16));
+#pragma unroll
+        for (int part = 0; part < kOpParts; ++part) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                f[2 * e] -= bf16_lo(w[e]);
+                f[2 * e + 1] -= bf16_hi(w[e]);
+            }
+            o[part * chunks + c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
-        o[c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        o[chunks + c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     if (blockIdx.y != 0) return;
     __shared__ int s_id[kGTileM];
@@ -479,28 +582,39 @@ operand_kernel(const OperandParams p)
     __syncthreads();
     bool first = id >= 0;
     for (int j = 0; j < tid; ++j) first = first && s_id[j] != id;
-    const uint32_t mask = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_cnt[warp] = __popc(mask);
+    // rank blocks before this thread's, by a scan over the tile
+    const int mine = first ? (max(1, min(p.ranks ? p.ranks[id] : p.r_max, p.r_max)) + 15) / 16 : 0;
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+    }
+    if (lane == 31) s_cnt[warp] = at;
     __syncthreads();
-    int at = __popc(mask & ((1u << lane) - 1u)), total = 0;
+    int total = 0;
+    at -= mine;
     for (int w = 0; w < kGTileM / 32; ++w) {
         if (w < warp) at += s_cnt[w];
         total += s_cnt[w];
     }
-    if (first) p.lists[m * kGTileM + at] = id;
+    for (int b = 0; b < mine; ++b) p.lists[(size_t)m * kListMax + at + b] = id * 4 + b;
     if (tid == 0) p.list_len[m] = total;
 }
 
-// The columns of a tile: the smallest of rounds x columns (rounds of the grid over the SMs), where
-// narrow tiles pay for reading their operands from shared memory more often per product
-// once the products bound the call (more than one token tile).
+// The columns of a tile: the smallest of rounds x columns (rounds of the grid over the SMs) with
+// a penalty on narrow tiles, whose stages carry fewer weight bytes per turn of the ring and read
+// their operands from shared memory more often per product. A single round has no such choice
+// to make: there narrower tiles only bring in more SMs. (8192 x 28672, 16 tokens: 112
+// columns in two rounds 6.1 TB/s of weights, 16 columns in thirteen 1.9 TB/s.)
 int tile_cols(int NC, int mt, int sms, const int* choices, int n_choices, const float* cost)
 {
     int best = choices[0];
     double least = 0;
     for (int i = 0; i < n_choices; ++i) {
         const long long tiles = (long long)mt * ((NC + choices[i] - 1) / choices[i]);
-        const double v = (double)((tiles + sms - 1) / sms) * choices[i] * (mt > 1 ? cost[i] : 1.f);
+        const long long rounds = (tiles + sms - 1) / sms;
+        const double v = (double)rounds * choices[i] * (rounds > 1 || mt > 1 ? cost[i] : 1.f);
         if (i == 0 || v < least) {
             least = v;
             best = choices[i];
@@ -533,21 +647,21 @@ cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int gr
 size_t gated_operand_bytes(int M, int r_max)
 {
     const size_t r16 = (size_t)(r_max + 15) / 16 * 16;
-    return (size_t)2 * M * 2 * r16 * 2;
+    return (size_t)2 * M * kOpParts * r16 * 2;
 }
 size_t gated_list_bytes(int M)
 {
     const size_t mt = (size_t)(M + kGTileM - 1) / kGTileM;
-    return mt * (kGTileM + 1) * 4;
+    return mt * (kListMax + 1) * 4;
 }
 
-cudaError_t launch_gated_operands(const float* v, int parts, const lora_pool_t& pool, const lora_segments_t& seg, int M,
+cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
                                   void* ops, void* lists, cudaStream_t stream)
 {
     const int mt = (M + kGTileM - 1) / kGTileM;
     OperandParams p = {};
     p.v = v;
-    p.parts = parts;
+    p.planes = planes;
     p.plane = (long long)pool.n_slices * M * pool.r_max;
     p.tok_adapter = seg.tok_adapter;
     p.ranks = pool.ranks;
@@ -558,9 +672,9 @@ cudaError_t launch_gated_operands(const float* v, int parts, const lora_pool_t& 
     p.r16 = (pool.r_max + 15) / 16 * 16;
     p.ops = static_cast<uint16_t*>(ops);
     p.lists = static_cast<int32_t*>(lists);
-    p.list_len = p.lists + (size_t)mt * kGTileM;
+    p.list_len = p.lists + (size_t)mt * kListMax;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)mt, kOpParts, 1);
+    cfg.gridDim = dim3((unsigned)mt, kOpCtas, 1);
     cfg.blockDim = dim3(kOpThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -602,7 +716,11 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     p.stage_bytes = p.a_bytes + p.bn * 128;
     if (a.lora) {
         p.r16 = (a.r_max + 15) / 16 * 16;
-        const int need = (bwd ? 1 : 2) * p.a_bytes + (p.cols + 63) / 64 * p.r16 * 128;
+        // four rank blocks per stage where its pieces fit the builders' registers and a stage of
+        // the main sum, else two
+        p.parts = save ? 3 : 2;
+        p.ups = p.cols <= 128 && (p.parts == 2 || a_rows <= 64) ? 4 : 2;
+        const int need = (int)lora_b_offset(p) + (bwd ? p.cols * 128 : (p.cols + 63) / 64 * p.ups * 2048);
         if (need > p.stage_bytes) p.stage_bytes = (need + 1023) / 1024 * 1024;
     }
     // 16 KB behind the last stage: what the MMA may read past a short A tile
@@ -624,7 +742,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.ops = static_cast<const uint16_t*>(a.ops);
         p.B = static_cast<const uint16_t*>(a.B);
         p.lists = static_cast<const int32_t*>(a.lists);
-        p.list_len = p.lists + (size_t)p.mt * kGTileM;
+        p.list_len = p.lists + (size_t)p.mt * kListMax;
         p.tok_adapter = a.tok_adapter;
         p.ranks = a.ranks;
         p.n_adapters = a.n_adapters;

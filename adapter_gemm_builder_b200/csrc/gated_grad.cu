@@ -1,6 +1,6 @@
-// gated_grad.cu -- the gated feed-forward block's backward around its matrix product
-// (gated.cu): the element-wise part, read from the 8-bit checkpoints, and the adapters'
-// gradients.
+// gated_grad.cu -- the gated feed-forward block around its matrix products (gated.cu): the
+// backward's element-wise part, read from the 8-bit checkpoints, the shrinks of both directions
+// and the adapters' gradients.
 //
 //   dg = dh u act'(g),  du = dh act(g),  h = act(g) u          (g, u: act8.cuh)
 //   dA_s,a = x_a^T (s_a d_s B_s,a^T),  dB_s,a = (s_a x A_s,a)_a^T d_s
@@ -118,8 +118,8 @@ gated_point_kernel(const PointParams p)
 // ------------------------------------------------------------------ adapters' gradients
 //
 // A segmented sum of outer products over an adapter's tokens: G[l][j] = sum_t lng[t][l] op[t][j],
-// lng = x (dA, l along K) or d_s (dB, l along F), op = the bf16 halves hi + lo of s_a u or s_a v
-// that operand_kernel wrote (about 16 bits). On mma.sync m16n8k16: the tensor work is
+// lng = x (dA, l along K) or d_s (dB, l along F), op = the first two bf16 parts of s_a u or
+// s_a v that operand_kernel wrote (16 bits). On mma.sync m16n8k16: the tensor work is
 // 2 r times the long elements, small beside reading them, so HBM bounds it. A CTA owns 64
 // values of l of one adapter and slice and walks the adapter's tokens 64 at a time, gathered
 // by cp.async into three stages; both operands come out of [token][value] rows by transposing
@@ -130,11 +130,12 @@ constexpr int kOThreads = 128;
 constexpr int kOTok = 64;
 constexpr int kOL = 64;
 constexpr int kOStages = 3;
+constexpr int kOpParts = 3;  // parts per token of the operands; two are used
 
 struct OuterParams {
     const uint16_t* lng;
     long long lng_slice;
-    const uint16_t* ops;  // [2][M][hi r16 | lo r16]
+    const uint16_t* ops;  // [2][M][kOpParts][r16]
     uint16_t* out;        // dA [2][n][L][r_max] or dB [2][n][r_max][L]
     const int32_t* perm;
     const int32_t* indptr;
@@ -147,6 +148,7 @@ struct OuterParams {
 template <int CH>
 __device__ __forceinline__ uint32_t o_chunk(int t, int c)
 {
+    if (CH == 2) return (uint32_t)(t * 32 + ((c ^ ((t >> 2) & 1)) << 4));
     if (CH == 4) return (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
     return (uint32_t)(t * CH * 16 + ((c ^ (t & 7)) << 4));
 }
@@ -166,7 +168,7 @@ gated_outer_kernel(const OuterParams p)
     const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
     const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
     const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
-    const uint16_t* ops = p.ops + (size_t)s * p.M * (2 * R16);
+    const uint16_t* ops = p.ops + (size_t)s * p.M * (kOpParts * R16);
     const uint32_t base = ptx::smem_u32(smem);
     const int steps = (n_tok + kOTok - 1) / kOTok;
 
@@ -184,7 +186,7 @@ gated_outer_kernel(const OuterParams p)
             for (int i = 0; i < kOTok * kOpCh / kOThreads; ++i) {
                 const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * kOTok + t;
                 const bool in = pos < n_tok;
-                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
+                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (kOpParts * R16) + c * 8 : ops;
                 ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
             }
         }
@@ -256,6 +258,136 @@ gated_outer_kernel(const OuterParams p)
     }
 }
 
+// ------------------------------------------------------------------ shrink
+//
+// v[t][j] = sum_l lng[t][l] w[l][j] for both slices: x.A_a (w's rows are l, as A is stored) and
+// d_s.B_a^T (rows are j, as B is stored: no transposed copy of the pool). A CTA takes a tile row of the
+// segments (up to 64 tokens of one adapter), a slice and one of `planes` parts of L; the
+// parts' sums go to planes of v that operand_kernel adds in order, so no atomics. mma.sync
+// m16n8k16: the products are 2 r16 per element of lng, few beside reading it, so HBM bounds it.
+// A warp owns 16 tokens; 64 values of l at a time come by cp.async into three stages.
+
+struct ShrinkParams {
+    const uint16_t* lng;
+    long long lng_slice;
+    const uint16_t* w;  // A [2][n][L][r_max] or B [2][n][r_max][L]
+    float* v;           // [planes][2][M][r_max]
+    const int32_t* perm;
+    const int4* tiles;
+    int M, L, n_adapters, r_max, planes, steps;  // steps of 64 per plane
+};
+
+template <bool DOWN, int R16>
+__global__ void __launch_bounds__(kOThreads)
+gated_shrink_kernel(const ShrinkParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kLngBytes = kOTok * 128, kWBytes = R16 * 128, kStage = kLngBytes + kWBytes;
+    constexpr int kWCh = DOWN ? R16 / 8 : 8;  // 16-byte pieces of a w row
+    constexpr int kWRows = DOWN ? 64 : R16;
+    constexpr int kWPer = kWRows * kWCh / kOThreads;  // pieces per thread
+    constexpr int NT = R16 / 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int plane = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int4 tl = p.tiles[blockIdx.x];
+    const int a = tl.x, n_tok = min(tl.z, kOTok);
+    if (a < 0 || a >= p.n_adapters || n_tok <= 0) return;
+    const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
+    const uint16_t* w = p.w + ((size_t)s * p.n_adapters + a) * p.r_max * p.L;
+    const uint32_t base = ptx::smem_u32(smem);
+    const int k0 = plane * p.steps, k1 = min(k0 + p.steps, (p.L + 63) / 64);
+    // this thread's token rows
+    const uint16_t* rows[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = (tid >> 3) + 16 * i;
+        rows[i] = t < n_tok ? lng + (size_t)p.perm[tl.y + t] * p.L : nullptr;
+    }
+    auto fetch = [&](int k) {
+        if (k < k1) {
+            const uint32_t st = base + (uint32_t)((k - k0) % kOStages * kStage);
+            const int l0 = k * 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = (tid >> 3) + 16 * i, c = tid & 7;
+                const bool in = rows[i] && l0 + c * 8 < p.L;
+                ptx::cp_async16(st + o_chunk<8>(t, c), in ? rows[i] + l0 + c * 8 : lng, in ? 16 : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kWPer; ++i) {
+                const int idx = tid + i * kOThreads, t = idx / kWCh, c = idx % kWCh;
+                const bool in = DOWN ? l0 + t < p.L && c * 8 < p.r_max : t < p.r_max && l0 + c * 8 < p.L;
+                const uint16_t* src = DOWN ? w + (size_t)(l0 + t) * p.r_max + c * 8 : w + (size_t)t * p.L + l0 + c * 8;
+                ptx::cp_async16(st + kLngBytes + o_chunk<kWCh>(t, c), in ? src : w, in ? 16 : 0);
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    for (int k = 0; k < kOStages - 1; ++k) fetch(k0 + k);
+    for (int k = k0; k < k1; ++k) {
+        ptx::cp_async_wait<kOStages - 2>();
+        __syncthreads();  // the step's rows are here, and the previous step's are consumed
+        fetch(k + kOStages - 1);
+        if (warp * 16 >= n_tok) continue;
+        const uint32_t st = base + (uint32_t)((k - k0) % kOStages * kStage), sw = st + kLngBytes;
+        const int i = lane >> 3, rr = lane & 7;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t A[4];
+            ptx::ldsm_x4(st + o_chunk<8>(warp * 16 + (i & 1) * 8 + rr, ks * 2 + (i >> 1)), A[0], A[1], A[2], A[3]);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b[4];
+                if (DOWN)
+                    ptx::ldsm_x4_t(sw + o_chunk<kWCh>(ks * 16 + (i & 1) * 8 + rr, n + (i >> 1)), b[0], b[1], b[2], b[3]);
+                else
+                    ptx::ldsm_x4(sw + o_chunk<kWCh>((n + (i >> 1)) * 8 + rr, ks * 2 + (i & 1)), b[0], b[1], b[2], b[3]);
+                ptx::mma_bf16_16816(acc[n], A, b[0], b[1]);
+                ptx::mma_bf16_16816(acc[n + 1], A, b[2], b[3]);
+            }
+        }
+    }
+    ptx::cp_async_wait<0>();
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int t = warp * 16 + g + h * 8;
+        if (t >= n_tok) continue;
+        float* o = p.v + (((size_t)plane * 2 + s) * p.M + p.perm[tl.y + t]) * p.r_max;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (n * 8 < p.r_max)
+                *reinterpret_cast<float2*>(o + n * 8 + q * 2) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+    }
+}
+
+template <bool DOWN, int R16>
+cudaError_t launch_shrink(const ShrinkParams& p, int rows, cudaStream_t stream)
+{
+    const size_t smem = (size_t)kOStages * (kOTok * 128 + R16 * 128);
+    auto kern = gated_shrink_kernel<DOWN, R16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows, (unsigned)p.planes, 2);
+    cfg.blockDim = dim3(kOThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <bool LONG_ROWS, int R16>
 cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 {
@@ -308,6 +440,37 @@ cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora
                  : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_SILU, false>, p);
     return h ? cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, true>, p)
              : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, false>, p);
+}
+
+// Parts of L: about four CTAs per SM, at most eight planes, at least four steps of 64 each.
+int gated_shrink_planes(int M, int L, int n_adapters)
+{
+    const long long ctas = 2LL * max_tiles_for(M, n_adapters), want = 4LL * device_sm_count();
+    const long long n = (want + ctas - 1) / ctas, most = (L + 255) / 256;
+    const long long planes = n < most ? n : most;
+    return (int)(planes < 1 ? 1 : (planes > 8 ? 8 : planes));
+}
+
+cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, int L, int M, const lora_pool_t& pool,
+                                const lora_segments_t& seg, float* v, int planes, cudaStream_t stream)
+{
+    ShrinkParams p = {};
+    p.lng = static_cast<const uint16_t*>(lng);
+    p.lng_slice = lng_slice;
+    p.w = static_cast<const uint16_t*>(down ? pool.A : pool.B);
+    p.v = v;
+    p.perm = seg.perm;
+    p.tiles = reinterpret_cast<const int4*>(seg.tiles);
+    p.M = M;
+    p.L = L;
+    p.n_adapters = pool.n_adapters;
+    p.r_max = pool.r_max;
+    p.planes = planes;
+    p.steps = ((L + 63) / 64 + planes - 1) / planes;
+    const int rows = max_tiles_for(M, pool.n_adapters);
+    if (pool.r_max <= 16) return down ? launch_shrink<true, 16>(p, rows, stream) : launch_shrink<false, 16>(p, rows, stream);
+    if (pool.r_max == 32) return down ? launch_shrink<true, 32>(p, rows, stream) : launch_shrink<false, 32>(p, rows, stream);
+    return down ? launch_shrink<true, 64>(p, rows, stream) : launch_shrink<false, 64>(p, rows, stream);
 }
 
 cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,

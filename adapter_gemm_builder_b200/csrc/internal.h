@@ -70,13 +70,20 @@ cudaError_t launch_mxfp4_quantize(const void* W, int N, int K, uint8_t* Wp, uint
 cudaError_t launch_act8_compress(const void* x, int M, int N, const lora_act8_t& out, cudaStream_t stream);
 cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cudaStream_t stream);
 
-// The gated feed-forward block. launch_gated_operands turns `parts` planes of v
-// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes) and lists the adapters
-// of each 128-token tile (gated_list_bytes); with adapters it is the launch right before
-// launch_gated_gemm (gated.cu says why).
+// The gated feed-forward block. launch_gated_operands turns `planes` planes of v
+// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes: [2][M][3 parts][r16]) and
+// lists the rank blocks of each 128-token tile (gated_list_bytes). With adapters the launches
+// right before launch_gated_gemm are a shrink that waits for its predecessors before it lets
+// its dependents start, then launch_gated_operands (gated.cu says why).
+// launch_gated_shrink: `planes` (gated_shrink_planes) planes of v[s][t][j] = sum_l lng[s][t][l] w,
+// w = pool.A[s][a][l][j] (down: x.A) or pool.B[s][a][j][l] (else: d.B^T), lng_slice 0: both
+// slices read one lng (gated_grad.cu).
+int gated_shrink_planes(int M, int L, int n_adapters);
+cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, int L, int M, const lora_pool_t& pool,
+                                const lora_segments_t& seg, float* v, int planes, cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
-cudaError_t launch_gated_operands(const float* v, int parts, const lora_pool_t& pool, const lora_segments_t& seg, int M,
+cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
                                   void* ops, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
     bool backward;
@@ -90,7 +97,7 @@ struct GatedGemmArgs {
     bool lora;
     const void* ops;
     const void* lists;
-    const void* B;          // [2][n_adapters][r_max][F], backward: the transposed A [2][n_adapters][r_max][K]
+    const void* B;          // the pool's B, backward: its A
     const int32_t* tok_adapter;
     const int32_t* ranks;
     int n_adapters, r_max;
