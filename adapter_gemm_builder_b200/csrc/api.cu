@@ -159,20 +159,12 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 }
 
 // v = x.A (down) or d.B^T of both slices into planes at v, then its operands and the token tiles'
-// rank blocks. Decode-like batches (tiles of four tokens) of the forward take the cluster kernel,
-// which spreads a token's row over a cluster.
+// rank blocks.
 cudaError_t gated_operands(bool down, const void* lng, int64_t lng_slice, const lora_pool_t& pool,
                            const lora_segments_t& seg, int M, float* v, void* ops, void* lists, cudaStream_t s)
 {
-    const int L = down ? pool.h_in : pool.h_out;
-    int planes = gated_shrink_planes(M, L, pool.n_adapters);
-    cudaError_t e;
-    if (down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
-        planes = 1;
-        e = launch_sgmv(SGMV_SHRINK, lng, lng_slice, pool, seg, v, nullptr, s, false);
-    } else {
-        e = launch_gated_shrink(down, lng, lng_slice, L, M, pool, seg, v, planes, s);
-    }
+    const int L = down ? pool.h_in : pool.h_out, planes = gated_shrink_planes(M, L, pool.n_adapters);
+    const cudaError_t e = launch_gated_shrink(down, lng, lng_slice, L, M, pool, seg, v, planes, s);
     if (e != cudaSuccess) return e;
     return launch_gated_operands(v, planes, pool, seg, M, ops, lists, s);
 }
@@ -672,7 +664,6 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
         a.lists = w + l.lists;
         a.B = pool->B;
         a.tok_adapter = seg->tok_adapter;
-        a.ranks = pool->ranks;
         a.n_adapters = pool->n_adapters;
         a.r_max = pool->r_max;
     }
@@ -725,7 +716,6 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.lists = w + l.lists;
     a.B = pool->A;
     a.tok_adapter = seg->tok_adapter;
-    a.ranks = pool->ranks;
     a.n_adapters = pool->n_adapters;
     a.r_max = pool->r_max;
     if (launch_gated_gemm(a, s) != cudaSuccess) return LORA_ERR_CUDA;

@@ -13,22 +13,21 @@
 // and Wg, Wu [F][K] are read as they are, as the MMA's MN-major operand (no transposed copy).
 //
 // The LoRA term extends the sum of a tile. operand_kernel below lists, for every 128 tokens, the
-// rank blocks (16 ranks of an adapter) that any of them uses; `ups` blocks fill one more ring
-// stage per slice: s_a v of the tile's rows (zero in the blocks of other adapters) against the
-// blocks of B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is
-// stored). v is split into bf16 parts that add up in the accumulator: hi + lo (16 bits of v), and
-// a third part where checkpoints are written, so that no code flips by the rounding of v
-// (two parts flipped codes three times as often as the fp32 sums do). Those stages lie between the main
-// ones in the second half of a tile's sum: the builders have the next stage's data in
-// registers before its slot is free, so a stage costs the ring a shared-memory write, not a
-// trip to memory (one stage per adapter at the end of the tile, loaded when its slot was free,
-// had cost about 2 us each: 160 us for 36 tokens of 32 adapters, 37 us without adapters).
+// rank blocks (16 ranks of an adapter) that any of them uses; a step adds `ups` blocks of one
+// slice: s_a v of the tile's rows (zero in the blocks of other adapters) against the blocks of
+// B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is stored). v is split
+// into bf16 halves hi + lo that add up in the accumulator (16 bits of v). The steps have shared
+// memory of their own beside the ring and are spread between the main stages (in a CTA's first
+// tile over its second half, so that the shrink runs under the first half); the builders
+// have a step's data in registers before its buffer is free, and nothing that a load
+// depends on is fetched in the same step. (Steps in ring slots, loaded when the slot was free,
+// had cost the ring about 2 us each: 36 tokens of 32 adapters took 160 us, 37 us without them.)
 // Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
 // are sorted by adapter has few adapters per tile.
 //
 // Roles (576 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
 // chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..17 build
-// the LoRA stages. Two accumulators (512 TMEM columns), so a tile drains under the next one's
+// the LoRA steps. Two accumulators (512 TMEM columns), so a tile drains under the next one's
 // products. Every wait is bounded; on expiry the CTA records a status word, lets what it
 // issued land and leaves.
 #include <cuda.h>
@@ -46,15 +45,15 @@ namespace {
 constexpr int kGDrainWarps = 8;
 constexpr int kGProducer = kGDrainWarps, kGMma = kGProducer + 1, kGBuilder0 = kGMma + 1;
 constexpr int kGBuilders = 256;
-constexpr int kGMaxA = 8, kGMaxB = 4;        // 16-byte pieces of a LoRA stage per builder
+constexpr int kGMaxA = 4, kGMaxB = 4;        // 16-byte pieces of a LoRA step per builder
 constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
 constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 8;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
 constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
+constexpr int kGSmemShort = 192 * 1024;       // the same with fewer than 128 tokens
 constexpr int kGBarBytes = 512;
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
-constexpr int kOpParts = 3;                   // bf16 parts of v that operand_kernel writes
 constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);
 enum { kGFwd = 0, kGBwd = 1 };
 // status bits of the bounded waits
@@ -66,6 +65,7 @@ struct GatedParams {
     int bn, cols;     // accumulator columns of a tile; output columns of a tile (bn / 2 forward)
     int kb, kb_half;  // ring stages of a tile's main sum; backward: those of dg
     int stages, stage_bytes, a_bytes;
+    int smem;         // dynamic shared memory
     int act;
     uint16_t* out;    // h [M][F] or dX [M][K]
     uint8_t *g_codes, *g_scales, *u_codes, *u_scales;  // forward checkpoints or NULL
@@ -73,14 +73,14 @@ struct GatedParams {
     unsigned long long timeout_ns;
     int inject_stall;
     // LoRA
-    const uint16_t* ops;      // [2][M][kOpParts][r16]: s_a v in bf16 parts
+    const uint16_t* ops;      // [2][M][hi r16 | lo r16]: s_a v as bf16 halves
     const uint16_t* B;        // forward B [2][n_adapters][r_max][NC], backward A [2][n_adapters][NC][r_max]
-    const int32_t* lists;     // [mt][kListMax] rank blocks of a token tile: adapter * 4 + block
+    const int32_t* lists;     // [mt][kListMax] rank blocks of a token tile (see block_code)
     const int32_t* list_len;  // [mt]
-    int parts, ups;           // parts of v used, rank blocks per stage
     const int32_t* tok_adapter;
-    const int32_t* ranks;
     int n_adapters, r_max, r16;
+    int ups;                  // rank blocks per step
+    int lbufs, lora_bytes;    // step buffers behind the ring
 };
 
 // K-major operand, 128-byte rows, 128-byte swizzle: 8-row groups 1024 bytes apart.
@@ -100,6 +100,44 @@ __device__ __forceinline__ uint64_t g_desc_mn(uint32_t a, uint32_t atom)
 __device__ __forceinline__ uint32_t g_idesc(int n, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Bounded wait by one thread that sleeps between its probes.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status, int code,
+                                       unsigned long long limit, bool honor_abort)
+{
+    const unsigned long long t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait_ns(bar, parity, 20000)) {
+        if (honor_abort && *abort_flag) return false;
+        if (ptx::globaltimer() - t0 > limit) {
+            *abort_flag = 1;
+            atomicOr(status, code);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status, int code,
+                                         unsigned long long limit, bool honor_abort = true)
+{
+    return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status, code, limit, honor_abort);
+}
+// The same for a converged warp; every lane gets the same answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status, int code,
+                                          unsigned long long limit, bool honor_abort = true)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, parity, abort_flag, status, code, limit, honor_abort));
+}
+// The same for the warps of a role (n threads, named barrier id): one thread probes, the
+// others sleep at the barrier; all get the same answer.
+__device__ __forceinline__ bool wait_role(int id, int n, bool prober, uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* status, int code, unsigned long long limit)
+{
+    const bool bad = prober && !wait_bar(bar, parity, abort_flag, status, code, limit);
+    if (ptx::named_sync_or(id, n, bad)) return false;
+    if (!prober) ptx::mbar_try_wait(bar, parity);  // complete: every thread observes the phase itself
+    return true;
 }
 
 // act(g): x sigmoid(x), or x Phi(x) through the complementary error function (no
@@ -139,12 +177,24 @@ __device__ __forceinline__ void save_block(const float* v, int n, uint8_t* codes
     *scale = (uint8_t)E;
 }
 
-// LoRA stages of token tile m: `ups` rank blocks each, both slices.
-__device__ __forceinline__ int lora_stages(const GatedParams& p, int m) { return 2 * ((p.list_len[m] + p.ups - 1) / p.ups); }
-// Where a LoRA stage's B part begins: behind the operand's tiles of 64 columns.
-__host__ __device__ __forceinline__ uint32_t lora_b_offset(const GatedParams& p)
+// A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has.
+__device__ __forceinline__ int block_code(int adapter, int block, int live) { return adapter << 8 | block << 6 | live; }
+__device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
+__device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
+__device__ __forceinline__ int block_live(int u) { return u & 63; }
+constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
+// The main stage after which the LoRA steps of a CTA's tile begin to be spread.
+__device__ __forceinline__ int lora_first(const GatedParams& p, int t) { return t == (int)blockIdx.x ? p.kb / 2 : 0; }
+// LoRA steps of a token tile with this many rank blocks, both slices.
+__device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
+// Where a step's B part begins: behind the operand's tiles of 64 columns (four groups of 16:
+// ups of hi, ups of lo).
+__host__ __device__ __forceinline__ uint32_t lora_b_offset(const GatedParams& p) { return (uint32_t)(p.ups / 2 * p.a_bytes); }
+// K-major operand of 64-byte rows (32 columns), 64-byte swizzle.
+__device__ __forceinline__ uint64_t g_desc_k64(uint32_t a)
 {
-    return (uint32_t)((p.parts * p.ups + 3) / 4 * p.a_bytes);
+    return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)4 << 61);
 }
 
 template <int MODE, bool LORA>
@@ -155,14 +205,15 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t raw_u = ptx::smem_u32(smem_raw);
     const uint32_t base_u = (raw_u + 1023u) & ~1023u;
     uint8_t* ring = smem_raw + (base_u - raw_u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + kGSmem - kGBarBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + p.smem - kGBarBytes);
     uint64_t* empty = full + kGMaxStages;
-    uint64_t* go = empty + kGMaxStages;  // the stage is free for the builders
-    uint64_t* tfull = go + kGMaxStages;
+    uint64_t* lfull = empty + kGMaxStages;  // [2] LoRA step buffers
+    uint64_t* lempty = lfull + 2;           // [2]
+    uint64_t* tfull = lempty + 2;
     uint64_t* tempty = tfull + 2;
     uint64_t* mdone = tempty + 2;
     uint64_t* stall = mdone + 1;  // test hook: never completed
@@ -174,9 +225,10 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         for (int s = 0; s < kGMaxStages; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
-            ptx::mbar_init(&go[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&lfull[b], 1);
+            ptx::mbar_init(&lempty[b], 1);
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], kGDrainWarps);
         }
@@ -204,13 +256,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         if (lane == 0) {
             int st = 0;
             uint32_t use = 0;            // uses of stage st before this one (all stages below st: one more)
-            int last[kGMaxStages];       // parity of the stage's last TMA fill, -1 if a builder filled it last
-            for (int s = 0; s < kGMaxStages; ++s) last[s] = -1;
             bool ok = true;
             if (p.inject_stall && blockIdx.x == 0)  // test hook: a wait that runs out
-                ok = wait_one<false>(stall, 0, abort_flag, status, kGStStall, p.timeout_ns);
+                ok = wait_bar(stall, 0, abort_flag, status, kGStStall, p.timeout_ns);
             auto acquire = [&]() {
-                return use == 0 || wait_one<false>(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
+                return use == 0 || wait_bar(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
             };
             auto next = [&]() {
                 if (++st == p.stages) {
@@ -218,16 +268,12 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     ++use;
                 }
             };
-            bool waited = false;
-            const int first = p.kb / 2;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
                 const int m = t % p.mt, n0 = (t / p.mt) * p.cols;
-                int ext = 0, acc = 0;  // LoRA stages of the tile, spread over its second half
-                for (int kb = 0; kb < p.kb && ok; ++kb) {
+                for (int kb = 0; kb < p.kb; ++kb) {
                     if (!(ok = acquire())) break;
                     const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
                     ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(p.a_bytes + p.bn * 128));
-                    last[st] = (int)(use & 1);
                     if (MODE == kGFwd) {
                         ptx::tma_load_2d(sa, &tmA0, &full[st], kb * kGKBlock, m * kGTileM);
                         ptx::tma_load_2d(sb, &tmB0, &full[st], kb * kGKBlock, n0);
@@ -240,210 +286,217 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             ptx::tma_load_2d(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, &full[st], n0 + b * 64, f0);
                     }
                     next();
-                    if (LORA && kb >= first) {
-                        if (kb == first) {
-                            if (!waited) ptx::pdl_wait();
-                            waited = true;
-                            ext = lora_stages(p, m);
-                        }
-                        for (acc += ext; acc >= p.kb - first; acc -= p.kb - first) {
-                            if (!(ok = acquire())) break;
-                            last[st] = -1;
-                            ptx::mbar_arrive(&go[st]);
-                            next();
-                        }
-                    }
                 }
             }
-            if (!ok)  // let every copy this CTA issued land before it leaves
-                for (int s = 0; s < p.stages; ++s)
-                    if (last[s] >= 0)
-                        wait_one<false, false>(&full[s], (uint32_t)last[s], abort_flag, status, kGStRing, p.timeout_ns);
+            // every copy this CTA issued lands before it leaves: the last fill of each stage
+            for (int s = 0; s < p.stages; ++s) {
+                const uint32_t fills = use + (s < st ? 1 : 0);
+                if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
+            }
         }
     } else if (warp == kGMma) {
         // ================================================================ MMA issuer
-        if (lane == 0) {
-            int st = 0, acc = 0;
-            uint32_t use = 0;
-            bool ok = true, waited = false;
-            const int first = p.kb / 2;
-            auto next = [&]() {
-                if (++st == p.stages) {
-                    st = 0;
-                    ++use;
-                }
-            };
-            const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, MODE == kGFwd);
-            const uint32_t lora_b = lora_b_offset(p);
-            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++acc) {
-                const int m = t % p.mt, buf = acc & 1;
-                if (acc >= 2 &&
-                    !(ok = wait_one<false>(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
-                                           p.timeout_ns)))
-                    break;
-                const uint32_t d = tmem + (uint32_t)(buf * kGAccCols);
-                int ext = 0, acc_e = 0, e = 0, blocks = 0;
-                for (int kb = 0; kb < p.kb && ok; ++kb) {
-                    if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+        // The whole warp walks the ring and one lane issues: what the descriptors are made of stays
+        // in uniform registers. (With the walk inside a lane-0 branch, an issue of four MMAs took
+        // longer than their 512 cycles of products: 2048 x 8192 x 11008 with adapters 645 us.)
+        const bool leader = ptx::elect_one();
+        int st = 0, acc = 0;
+        uint32_t use = 0, step = 0;  // turns of the ring; LoRA steps so far
+        bool ok = true, waited = false;
+        const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, MODE == kGFwd);
+        // descriptors of stage 0 and of LoRA buffer 0; the address field counts 16-byte units
+        const uint32_t lora_u = base_u + (uint32_t)(p.stages * p.stage_bytes), lora_bu = lora_u + lora_b_offset(p);
+        const uint64_t da0 = g_desc_k(base_u);
+        const uint64_t db0 = MODE == kGFwd ? g_desc_k(base_u + (uint32_t)p.a_bytes) : g_desc_mn(base_u + (uint32_t)p.a_bytes, 8192);
+        const uint64_t la0 = g_desc_k(lora_u);
+        const uint64_t lb0 = MODE == kGFwd ? g_desc_mn(lora_bu, (uint32_t)(p.ups * 2048)) : g_desc_k64(lora_bu);
+        const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4;
+        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++acc) {
+            const int m = t % p.mt, buf = acc & 1;
+            const int first = lora_first(p, t), spread = p.kb - first;
+            int blocks = LORA && waited ? p.list_len[m] : 0;
+            if (acc >= 2 && !(ok = wait_warp(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
+                                             p.timeout_ns)))
+                break;
+            const uint32_t d = tmem + (uint32_t)(buf * kGAccCols);
+            // main stages [kb, stop) of the tile
+            auto main_stages = [&](int kb, int stop) {
+                for (; kb < stop; ++kb) {
+                    if (!(ok = wait_warp(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
                     ptx::tc_fence_after();
-                    const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+                    if (leader) {
+                        const uint64_t da = da0 + (uint32_t)st * stage16, db = db0 + (uint32_t)st * stage16;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        ptx::tc_mma_f16(d, g_desc_k(sa + (uint32_t)(ks * 32)),
-                                        MODE == kGFwd ? g_desc_k(sb + (uint32_t)(ks * 32))
-                                                      : g_desc_mn(sb + (uint32_t)(ks * 2048), 8192),
-                                        id_main, (kb | ks) ? 1u : 0u);
-                    ptx::tc_commit(&empty[st]);
-                    next();
-                    if (LORA && kb >= first) {
-                        if (kb == first) {
-                            if (!waited) ptx::pdl_wait();
-                            waited = true;
-                            blocks = p.list_len[m];
-                            ext = lora_stages(p, m);
-                        }
-                        for (acc_e += ext; acc_e >= p.kb - first; acc_e -= p.kb - first, ++e) {
-                            if (!(ok = wait_one<false>(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
-                            ptx::tc_fence_after();
-                            const uint32_t la = base_u + (uint32_t)(st * p.stage_bytes), lb = la + lora_b;
-                            const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
-                            const int n = min(p.ups, blocks - (e >> 1) * p.ups);
-                            for (int part = 0; part < p.parts; ++part)
-                                for (int k = 0; k < n; ++k) {
-                                    const int c = part * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
-                                    ptx::tc_mma_f16(ds, g_desc_k(la + (uint32_t)((c >> 2) * p.a_bytes + (c & 3) * 32)),
-                                                    MODE == kGFwd ? g_desc_mn(lb + (uint32_t)(k * 2048), (uint32_t)(p.ups * 2048))
-                                                                  : g_desc_k(lb + (uint32_t)(k * 32)),
-                                                    id_lora, 1u);
-                                }
-                            ptx::tc_commit(&empty[st]);
-                            next();
-                        }
+                        for (int ks = 0; ks < 4; ++ks)
+                            ptx::tc_mma_f16_all(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, (kb | ks) ? 1u : 0u);
+                        ptx::tc_commit(&empty[st]);
+                    }
+                    __syncwarp();
+                    if (++st == p.stages) {
+                        st = 0;
+                        ++use;
                     }
                 }
-                if (ok) ptx::tc_commit(&tfull[buf]);
+            };
+            if (!LORA) {
+                main_stages(0, p.kb);
+            } else {
+                // the tile's LoRA steps, evenly between the main stages from `first` on
+                int kb = first + 1, e = 0;
+                main_stages(0, kb);
+                if (ok && !waited) {
+                    ptx::pdl_wait();
+                    waited = true;
+                    blocks = p.list_len[m];
+                }
+                blocks = __shfl_sync(0xffffffffu, blocks, 0);  // uniform, and so the walk
+                const int ext = lora_steps(p, blocks);
+                int due = ext;
+                while (ok) {
+                    for (; due >= spread; due -= spread, ++e, ++step) {
+                        const uint32_t lb = p.lbufs == 2 ? step & 1 : 0, turn = p.lbufs == 2 ? step >> 1 : step;
+                        if (!(ok = wait_warp(&lfull[lb], turn & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+                        ptx::tc_fence_after();
+                        if (leader) {
+                            const uint32_t at = lb * ((uint32_t)p.lora_bytes >> 4);
+                            const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
+                            const int n = min(p.ups, blocks - (e >> 1) * p.ups);
+                            for (int h = 0; h < 2; ++h)
+                                for (int k = 0; k < n; ++k) {
+                                    const int c = h * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
+                                    ptx::tc_mma_f16_all(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
+                                                    lb0 + at + (uint32_t)(k * (MODE == kGFwd ? 128 : 2)), id_lora, 1u);
+                                }
+                            ptx::tc_commit(&lempty[lb]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok || kb >= p.kb) break;
+                    const int n = ext ? min((spread - due + ext - 1) / ext, p.kb - kb) : p.kb - kb;
+                    main_stages(kb, kb + n);
+                    kb += n;
+                    due += n * ext;
+                }
             }
-            // every MMA issued is complete before the CTA leaves
-            ptx::tc_commit(mdone);
-            wait_one<false, false>(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns);
+            if (ok && leader) ptx::tc_commit(&tfull[buf]);
+            __syncwarp();
         }
+        // every MMA issued is complete before the CTA leaves
+        if (leader) ptx::tc_commit(mdone);
+        __syncwarp();
+        wait_warp(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns, false);
     } else if (warp >= kGBuilder0) {
-        // ================================================================ LoRA stages
+        // ================================================================ LoRA steps
         if (LORA) {
             ptx::pdl_wait();
             const int bt = threadIdx.x - kGBuilder0 * 32;
-            const int first = p.kb / 2, spread = p.kb - first;
             // A builder's pieces lie in one column of 16-byte pieces, a fixed number of rows apart
             // (a multiple of eight, so their swizzle is the same): piece i of the operand in row
-            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c.
-            const int a_cpr = 2 * p.ups * p.parts, a_lg = a_cpr <= 8 ? 3 : (a_cpr <= 16 ? 4 : 5);
-            const int a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
-            const int a_rows = a_c < a_cpr ? p.a_bytes >> 7 : 0;
-            const int b_cpr = MODE == kGFwd ? p.cols >> 3 : 2 * p.ups, b_lg = MODE == kGFwd ? 4 : (p.ups == 4 ? 3 : 2);
-            const int b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
-            const int b_rows = b_c < b_cpr ? (MODE == kGFwd ? 16 * p.ups : p.cols) : 0;
-            const int a_part = a_c / (2 * p.ups), a_k = a_c - a_part * 2 * p.ups;
+            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c. Forward, a pass of
+            // B's rows is one rank block (b_step 16).
+            const int a_lg = p.ups == 4 ? 4 : 3, a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
+            const int a_rows = p.a_bytes >> 7;
+            const int a_half = a_c >> (a_lg - 1), a_k = a_c & ((1 << (a_lg - 1)) - 1);  // hi or lo; piece of the blocks
+            const int b_lg = MODE == kGFwd ? 4 : 2, b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
+            const int b_rows = MODE == kGFwd ? (b_c < p.cols >> 3 ? 16 * p.ups : 0) : p.cols;
             const uint32_t a_off = (uint32_t)((a_c >> 3) * p.a_bytes + a_row * 128 + (((a_c & 7) ^ (a_row & 7)) << 4));
-            const uint32_t b_off = (uint32_t)((MODE == kGFwd ? (b_c >> 3) * (p.ups * 2048) : 0) + b_row * 128 +
-                                              (((b_c & 7) ^ (b_row & 7)) << 4));
-            const uint32_t lora_b = lora_b_offset(p);
-            // the walk over the ring: main stages are passed over, LoRA stages stopped at
-            int t = blockIdx.x, st = 0, k = 0, acc = 0, ext = 0, e = -1;
-            bool open = false, main_done = false;
-            int m = 0, n0 = 0;
-            auto advance = [&]() -> bool {  // to the next LoRA stage: (m, n0, e) in slot st
-                for (; t < p.tiles; t += gridDim.x, open = false) {
+            const uint32_t b_off =
+                lora_b_offset(p) + (MODE == kGFwd ? (uint32_t)((b_c >> 3) * (p.ups * 2048) + b_row * 128 + (((b_c & 7) ^ (b_row & 7)) << 4))
+                                                  : (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4)));
+            uint8_t* bufs = ring + p.stages * p.stage_bytes;
+
+            // the walk over the steps: tile t, its step e of `ext`
+            int t = blockIdx.x, e = -1, ext = 0, m = 0, n0 = 0, blocks = 0;
+            bool open = false;
+            int ids[kGMaxA];  // adapters of this builder's operand rows
+            auto advance = [&]() -> bool {
+                for (;; t += gridDim.x, open = false) {
+                    if (t >= p.tiles) return false;
                     if (!open) {
                         m = t % p.mt;
                         n0 = (t / p.mt) * p.cols;
-                        ext = lora_stages(p, m);
-                        st = (st + (ext ? first : p.kb)) % p.stages;
-                        k = ext ? 0 : spread;
-                        acc = 0;
+                        blocks = p.list_len[m];
+                        ext = lora_steps(p, blocks);
                         e = -1;
                         open = true;
-                        main_done = false;
-                    } else if (e >= 0) {
-                        if (++st == p.stages) st = 0;  // past the LoRA stage stopped at
-                    }
-                    for (; k < spread; ++k, main_done = false) {
-                        if (!main_done) {
-                            if (++st == p.stages) st = 0;
-                            acc += ext;
-                            main_done = true;
-                        }
-                        if (acc >= spread) {
-                            acc -= spread;
-                            ++e;
-                            return true;
+#pragma unroll
+                        for (int i = 0; i < kGMaxA; ++i) {
+                            const int row = a_row + i * a_step, tok = m * kGTileM + row;
+                            ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
                         }
                     }
+                    if (++e < ext) return true;
                 }
-                return false;
+            };
+            // the blocks that the next step's pieces come from: one for the operand, one per pass of B
+            int ua, ub[kGMaxB];
+            auto blocks_of_step = [&]() {
+                const int b0 = (e >> 1) * p.ups;
+                const int32_t* list = p.lists + (size_t)m * kListMax;
+                const int ka = b0 + (a_k >> 1);
+                ua = ka < blocks ? list[ka] : kNoBlock;
+#pragma unroll
+                for (int i = 0; i < kGMaxB; ++i) {
+                    const int kb = b0 + (MODE == kGFwd ? i : b_c >> 1);
+                    ub[i] = (MODE == kGFwd ? i < p.ups : i == 0) && kb < blocks ? list[kb] : kNoBlock;
+                }
             };
             uint4 ra[kGMaxA], rb[kGMaxB];
-            auto load = [&]() {  // the stage's pieces into registers; zero where nothing belongs
-                const int s = e & 1, b0 = (e >> 1) * p.ups;
-                const int32_t* list = p.lists + (size_t)m * kListMax;
-                const int blocks = p.list_len[m];
-                {
-                    const int u = b0 + (a_k >> 1) < blocks ? list[b0 + (a_k >> 1)] : -4;
-                    const size_t at = ((size_t)s * p.M * kOpParts + a_part) * p.r16 + (u & 3) * 16 + (a_k & 1) * 8;
+            auto load = [&]() {  // the step's pieces into registers; zero where nothing belongs
+                const int s = e & 1;
+                const uint16_t* src = p.ops + (size_t)s * p.M * (2 * p.r16) + a_half * p.r16 + block_rank0(ua) + (a_k & 1) * 8;
 #pragma unroll
-                    for (int i = 0; i < kGMaxA; ++i) {
-                        const int row = a_row + i * a_step, tok = m * kGTileM + row;
-                        ra[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < a_rows && tok < p.M && u >= 0 && p.tok_adapter[tok] == (u >> 2))
-                            ra[i] = *reinterpret_cast<const uint4*>(p.ops + at + (size_t)tok * (kOpParts * p.r16));
-                    }
+                for (int i = 0; i < kGMaxA; ++i) {
+                    ra[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (ids[i] == block_adapter(ua))
+                        ra[i] = *reinterpret_cast<const uint4*>(src + (size_t)(m * kGTileM + a_row + i * a_step) * (2 * p.r16));
                 }
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i) {
-                    const int row = b_row + i * b_step, b = b0 + (MODE == kGFwd ? row >> 4 : b_c >> 1);
+                    const int row = b_row + i * b_step, u = MODE == kGFwd ? ub[i] : ub[0];
                     rb[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row >= b_rows || b >= blocks) continue;
-                    const int u = list[b], a = u >> 2;
-                    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
-                    const uint16_t* src = p.B + ((size_t)s * p.n_adapters + a) * p.r_max * p.NC;
-                    if (MODE == kGFwd) {  // row j of B_a, eight columns
-                        const int j = (u & 3) * 16 + (row & 15);
-                        if (j < r && n0 + b_c * 8 < p.NC)
-                            rb[i] = *reinterpret_cast<const uint4*>(src + (size_t)j * p.NC + n0 + b_c * 8);
-                    } else {  // row n of A_a, eight ranks; what lies past the rank is not read as a number
-                        const int j = (u & 3) * 16 + (b_c & 1) * 8, live = r - j;
-                        if (live > 0 && n0 + row < p.NC) {
-                            rb[i] = *reinterpret_cast<const uint4*>(src + (size_t)(n0 + row) * p.r_max + j);
-                            if (live < 8) {
-                                uint32_t* w = reinterpret_cast<uint32_t*>(&rb[i]);
-#pragma unroll
-                                for (int h = 0; h < 4; ++h)
-                                    w[h] &= live > 2 * h + 1 ? 0xffffffffu : (live > 2 * h ? 0xffffu : 0u);
-                            }
-                        }
+                    const size_t pool = ((size_t)s * p.n_adapters + block_adapter(u)) * p.r_max * p.NC;
+                    if (MODE == kGFwd) {  // a row of B_a, eight columns
+                        if (row < b_rows && b_row < block_live(u) && n0 + b_c * 8 < p.NC)
+                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(block_rank0(u) + b_row) * p.NC + n0 + b_c * 8);
+                    } else {  // a row of A_a, eight ranks
+                        const int j = (b_c & 1) * 8;
+                        if (row < b_rows && j < block_live(u) && n0 + row < p.NC)
+                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(n0 + row) * p.r_max + block_rank0(u) + j);
                     }
                 }
             };
-            uint32_t gos = 0;  // bit s: parity of the next `go` of slot s
             bool more = advance();
-            if (more) load();
-            while (more) {
-                // all builders take part or none (a wait that ran out may show in one warp only)
-                bool ok = wait_all<false>(&go[st], (gos >> st) & 1, abort_flag, status, kGStBuild, p.timeout_ns);
-                ok = !ptx::named_sync_or(1, kGBuilders, !ok);
-                if (!ok) break;
-                gos ^= 1u << st;
-                uint8_t *sa = ring + st * p.stage_bytes + a_off, *sb = ring + st * p.stage_bytes + lora_b + b_off;
+            if (more) {
+                blocks_of_step();
+                load();
+            }
+            for (uint32_t step = 0; more; ++step) {
+                const uint32_t lb = p.lbufs == 2 ? step & 1 : 0, turn = p.lbufs == 2 ? step >> 1 : step;
+                const int last = MODE == kGBwd ? block_live(ub[0]) - (b_c & 1) * 8 : 8;  // ranks of the pieces of A_a that count
+                more = advance();
+                if (more) blocks_of_step();
+                if (turn > 0 && !wait_role(1, kGBuilders, bt == 0, &lempty[lb], (turn - 1) & 1, abort_flag, status, kGStBuild,
+                                           p.timeout_ns))
+                    break;
+                uint8_t *sa = bufs + lb * p.lora_bytes + a_off, *sb = bufs + lb * p.lora_bytes + b_off;
 #pragma unroll
                 for (int i = 0; i < kGMaxA; ++i)
                     if (a_row + i * a_step < a_rows) *reinterpret_cast<uint4*>(sa + i * a_step * 128) = ra[i];
 #pragma unroll
-                for (int i = 0; i < kGMaxB; ++i)
-                    if (b_row + i * b_step < b_rows) *reinterpret_cast<uint4*>(sb + i * b_step * 128) = rb[i];
+                for (int i = 0; i < kGMaxB; ++i) {
+                    if (MODE == kGBwd && last < 8) {  // what lies past the rank is not a number
+                        uint32_t* w = reinterpret_cast<uint32_t*>(&rb[i]);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) w[h] &= last > 2 * h + 1 ? 0xffffffffu : (last > 2 * h ? 0xffffu : 0u);
+                    }
+                    if (b_row + i * b_step < b_rows)
+                        *reinterpret_cast<uint4*>(sb + i * b_step * (MODE == kGFwd ? 128 : 64)) = rb[i];
+                }
                 ptx::fence_proxy_async_smem();
+                if (more) load();  // in flight over the barrier and the next wait
                 ptx::named_sync(2, kGBuilders);
-                if (bt == 0) ptx::mbar_arrive(&full[st]);
-                more = advance();
-                if (more) load();
+                if (bt == 0) ptx::mbar_arrive(&lfull[lb]);
             }
         }
     } else {
@@ -453,7 +506,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++acc) {
             const int m = t % p.mt, n0 = (t / p.mt) * p.cols, buf = acc & 1;
             const int row = m * kGTileM + q * 32 + lane;
-            if (!wait_all<false>(&tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status, kGStDrain, p.timeout_ns)) break;
+            if (!wait_role(3, kGDrainWarps * 32, threadIdx.x == 0, &tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status,
+                           kGStDrain, p.timeout_ns))
+                break;
             ptx::tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGAccCols);
             if (m * kGTileM + q * 32 < p.M) {  // the warp has live rows
@@ -528,8 +583,7 @@ struct OperandParams {
 constexpr int kOpThreads = 128;
 constexpr int kOpCtas = 8;  // CTAs per token tile, 16 rows each
 
-// s_a v of both slices in kOpParts bf16 parts that add up to it (columns past the rank zero),
-// and per token tile the rank blocks that its rows use, adapters in order of first appearance.
+// s_a v of both slices as bf16 halves hi + lo (columns past the rank zero), and per token tile the rank blocks that its rows use, adapters in order of first appearance.
 // Lets the GEMM start at once (see the wait there).
 __global__ void __launch_bounds__(kOpThreads)
 operand_kernel(const OperandParams p)
@@ -559,9 +613,9 @@ operand_kernel(const OperandParams p)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
-        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (kOpParts * p.r16));
+        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
 #pragma unroll
-        for (int part = 0; part < kOpParts; ++part) {
+        for (int part = 0; part < 2; ++part) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -583,7 +637,7 @@ operand_kernel(const OperandParams p)
     bool first = id >= 0;
     for (int j = 0; j < tid; ++j) first = first && s_id[j] != id;
     // rank blocks before this thread's, by a scan over the tile
-    const int mine = first ? (max(1, min(p.ranks ? p.ranks[id] : p.r_max, p.r_max)) + 15) / 16 : 0;
+    const int rank = first ? max(1, min(p.ranks ? p.ranks[id] : p.r_max, p.r_max)) : 0, mine = (rank + 15) / 16;
     int at = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -598,7 +652,7 @@ operand_kernel(const OperandParams p)
         if (w < warp) at += s_cnt[w];
         total += s_cnt[w];
     }
-    for (int b = 0; b < mine; ++b) p.lists[(size_t)m * kListMax + at + b] = id * 4 + b;
+    for (int b = 0; b < mine; ++b) p.lists[(size_t)m * kListMax + at + b] = block_code(id, b, min(16, rank - 16 * b));
     if (tid == 0) p.list_len[m] = total;
 }
 
@@ -632,7 +686,7 @@ cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int gr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(kGThreads, 1, 1);
-    cfg.dynamicSmemBytes = kGSmem;
+    cfg.dynamicSmemBytes = (size_t)p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -647,7 +701,7 @@ cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int gr
 size_t gated_operand_bytes(int M, int r_max)
 {
     const size_t r16 = (size_t)(r_max + 15) / 16 * 16;
-    return (size_t)2 * M * kOpParts * r16 * 2;
+    return (size_t)2 * M * 2 * r16 * 2;
 }
 size_t gated_list_bytes(int M)
 {
@@ -714,17 +768,21 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     const int a_rows = a.M >= kGTileM ? kGTileM : (a.M + 7) / 8 * 8;
     p.a_bytes = a_rows * 128;
     p.stage_bytes = p.a_bytes + p.bn * 128;
+    // Full token tiles take all shared memory. Fewer tokens leave some of it, so that the small
+    // kernels before this one keep running beside its CTAs (which then start at once, the
+    // weights streaming under the shrink); their 16 KB at the end are what the MMA may read past a
+    // short operand tile.
+    int room = (a_rows < kGTileM ? kGSmemShort - kGTileM * 128 : kGSmem) - kGBarBytes - 1024;
+    p.smem = a_rows < kGTileM ? kGSmemShort : kGSmem;
     if (a.lora) {
         p.r16 = (a.r_max + 15) / 16 * 16;
-        // four rank blocks per stage where its pieces fit the builders' registers and a stage of
-        // the main sum, else two
-        p.parts = save ? 3 : 2;
-        p.ups = p.cols <= 128 && (p.parts == 2 || a_rows <= 64) ? 4 : 2;
-        const int need = (int)lora_b_offset(p) + (bwd ? p.cols * 128 : (p.cols + 63) / 64 * p.ups * 2048);
-        if (need > p.stage_bytes) p.stage_bytes = (need + 1023) / 1024 * 1024;
+        // rank blocks per step: what four pieces per builder and the space beside four stages hold
+        p.ups = !bwd && a_rows <= 64 ? 4 : 2;
+        p.lora_bytes = (int)lora_b_offset(p) + (bwd ? p.cols * 64 : (p.cols + 63) / 64 * p.ups * 2048);
+        p.lora_bytes = (p.lora_bytes + 1023) / 1024 * 1024;
+        p.lbufs = room - 2 * p.lora_bytes >= 4 * p.stage_bytes ? 2 : 1;
+        room -= p.lbufs * p.lora_bytes;
     }
-    // 16 KB behind the last stage: what the MMA may read past a short A tile
-    const int room = kGSmem - kGBarBytes - 1024 - (a_rows < kGTileM ? kGTileM * 128 : 0);
     p.stages = room / p.stage_bytes;
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
     p.act = a.act;
@@ -744,7 +802,6 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.lists = static_cast<const int32_t*>(a.lists);
         p.list_len = p.lists + (size_t)p.mt * kListMax;
         p.tok_adapter = a.tok_adapter;
-        p.ranks = a.ranks;
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
     }

@@ -118,7 +118,7 @@ gated_point_kernel(const PointParams p)
 // ------------------------------------------------------------------ adapters' gradients
 //
 // A segmented sum of outer products over an adapter's tokens: G[l][j] = sum_t lng[t][l] op[t][j],
-// lng = x (dA, l along K) or d_s (dB, l along F), op = the first two bf16 parts of s_a u or
+// lng = x (dA, l along K) or d_s (dB, l along F), op = the bf16 halves hi + lo of s_a u or
 // s_a v that operand_kernel wrote (16 bits). On mma.sync m16n8k16: the tensor work is
 // 2 r times the long elements, small beside reading them, so HBM bounds it. A CTA owns 64
 // values of l of one adapter and slice and walks the adapter's tokens 64 at a time, gathered
@@ -130,12 +130,11 @@ constexpr int kOThreads = 128;
 constexpr int kOTok = 64;
 constexpr int kOL = 64;
 constexpr int kOStages = 3;
-constexpr int kOpParts = 3;  // parts per token of the operands; two are used
 
 struct OuterParams {
     const uint16_t* lng;
     long long lng_slice;
-    const uint16_t* ops;  // [2][M][kOpParts][r16]
+    const uint16_t* ops;  // [2][M][hi r16 | lo r16]
     uint16_t* out;        // dA [2][n][L][r_max] or dB [2][n][r_max][L]
     const int32_t* perm;
     const int32_t* indptr;
@@ -168,7 +167,7 @@ gated_outer_kernel(const OuterParams p)
     const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
     const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
     const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
-    const uint16_t* ops = p.ops + (size_t)s * p.M * (kOpParts * R16);
+    const uint16_t* ops = p.ops + (size_t)s * p.M * (2 * R16);
     const uint32_t base = ptx::smem_u32(smem);
     const int steps = (n_tok + kOTok - 1) / kOTok;
 
@@ -186,7 +185,7 @@ gated_outer_kernel(const OuterParams p)
             for (int i = 0; i < kOTok * kOpCh / kOThreads; ++i) {
                 const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * kOTok + t;
                 const bool in = pos < n_tok;
-                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (kOpParts * R16) + c * 8 : ops;
+                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
                 ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
             }
         }
@@ -368,6 +367,64 @@ gated_shrink_kernel(const ShrinkParams p)
     }
 }
 
+// The down shrink of a decode-like batch: a CTA takes a token, a slice and a plane's part of
+// L; a thread sums eight ranks over every (128 / pieces)-th l, the rows of A_a as they come. Small
+// enough (no shared memory to speak of) to run beside the CTAs of the GEMM, whose weights
+// stream meanwhile.
+__global__ void __launch_bounds__(kOThreads)
+gated_shrink_token_kernel(const ShrinkParams p, const int32_t* __restrict__ tok_adapter)
+{
+    __shared__ float s_sum[kOThreads / 32][LORA_MAX_RANK];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int t = (int)blockIdx.x, plane = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int a = tok_adapter[t];
+    if (a < 0 || a >= p.n_adapters) return;
+    const uint16_t* x = p.lng + (size_t)s * p.lng_slice + (size_t)t * p.L;
+    const uint16_t* w = p.w + ((size_t)s * p.n_adapters + a) * p.r_max * p.L;
+    const int pieces = p.r_max >> 3, c = tid & (pieces - 1), step = kOThreads / pieces;
+    const int l1 = min((plane + 1) * p.steps * 64, p.L);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    constexpr int kAhead = 8;
+    for (int l = plane * p.steps * 64 + tid / pieces; l < l1; l += kAhead * step) {
+        uint4 wv[kAhead];
+        float xv[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int at = l + i * step;
+            wv[i] = make_uint4(0u, 0u, 0u, 0u);
+            xv[i] = 0.f;
+            if (at < l1) {
+                wv[i] = *reinterpret_cast<const uint4*>(w + (size_t)at * p.r_max + c * 8);
+                xv[i] = __uint_as_float((uint32_t)x[at] << 16);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t u[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[2 * e] = fmaf(xv[i], bf16_lo(u[e]), acc[2 * e]);
+                acc[2 * e + 1] = fmaf(xv[i], bf16_hi(u[e]), acc[2 * e + 1]);
+            }
+        }
+    }
+    for (int o = 16; o >= pieces; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+    if (lane < pieces)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[warp][c * 8 + e] = acc[e];
+    __syncthreads();
+    if (tid < p.r_max) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kOThreads / 32; ++i) v += s_sum[i][tid];
+        p.v[(((size_t)plane * 2 + s) * p.M + t) * p.r_max + tid] = v;
+    }
+}
+
 template <bool DOWN, int R16>
 cudaError_t launch_shrink(const ShrinkParams& p, int rows, cudaStream_t stream)
 {
@@ -467,6 +524,18 @@ cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, i
     p.r_max = pool.r_max;
     p.planes = planes;
     p.steps = ((L + 63) / 64 + planes - 1) / planes;
+    if (down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)M, (unsigned)planes, 2);
+        cfg.blockDim = dim3(kOThreads, 1, 1);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, gated_shrink_token_kernel, p, (const int32_t*)seg.tok_adapter);
+    }
     const int rows = max_tiles_for(M, pool.n_adapters);
     if (pool.r_max <= 16) return down ? launch_shrink<true, 16>(p, rows, stream) : launch_shrink<false, 16>(p, rows, stream);
     if (pool.r_max == 32) return down ? launch_shrink<true, 32>(p, rows, stream) : launch_shrink<false, 32>(p, rows, stream);

@@ -71,7 +71,7 @@ cudaError_t launch_act8_compress(const void* x, int M, int N, const lora_act8_t&
 cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cudaStream_t stream);
 
 // The gated feed-forward block. launch_gated_operands turns `planes` planes of v
-// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes: [2][M][3 parts][r16]) and
+// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
 // lists the rank blocks of each 128-token tile (gated_list_bytes). With adapters the launches
 // right before launch_gated_gemm are a shrink that waits for its predecessors before it lets
 // its dependents start, then launch_gated_operands (gated.cu says why).
@@ -99,7 +99,6 @@ struct GatedGemmArgs {
     const void* lists;
     const void* B;          // the pool's B, backward: its A
     const int32_t* tok_adapter;
-    const int32_t* ranks;
     int n_adapters, r_max;
 };
 // cudaErrorInvalidValue if an operand's tensor map is refused.
