@@ -160,13 +160,13 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 
 // v = x.A (down) or d.B^T of both slices into planes at v, then its operands and the token tiles'
 // rank blocks.
-cudaError_t gated_operands(bool down, const void* lng, int64_t lng_slice, const lora_pool_t& pool,
+cudaError_t gated_operands(bool down, bool save, const void* lng, int64_t lng_slice, const lora_pool_t& pool,
                            const lora_segments_t& seg, int M, float* v, void* ops, void* lists, cudaStream_t s)
 {
     const int L = down ? pool.h_in : pool.h_out, planes = gated_shrink_planes(M, L, pool.n_adapters);
     const cudaError_t e = launch_gated_shrink(down, lng, lng_slice, L, M, pool, seg, v, planes, s);
     if (e != cudaSuccess) return e;
-    return launch_gated_operands(v, planes, pool, seg, M, ops, lists, s);
+    return launch_gated_operands(v, planes, pool, seg, M, !down, save, ops, lists, s);
 }
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
@@ -657,7 +657,7 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
-        if (gated_operands(true, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
+        if (gated_operands(true, g8 != nullptr, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
             return LORA_ERR_CUDA;
         a.lora = true;
         a.ops = w + l.ops;
@@ -708,7 +708,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     if (!pool) return cuda_status(launch_gated_gemm(a, s));
     // 2. u = d.B^T of both slices
     float* v = reinterpret_cast<float*>(w + l.v);
-    if (gated_operands(false, dg, (int64_t)M * F, *pool, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess)
+    if (gated_operands(false, false, dg, (int64_t)M * F, *pool, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess)
         return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
@@ -724,7 +724,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
         if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
         x = w + l.x;
     }
-    if (gated_operands(true, x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
+    if (gated_operands(true, false, x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
         launch_gated_outer(true, x, 0, K, w + l.ops_u, M, *pool, *seg, dA, s) != cudaSuccess ||
         launch_gated_outer(false, dg, (int64_t)M * F, F, w + l.ops_v, M, *pool, *seg, dB, s) != cudaSuccess)
         return LORA_ERR_CUDA;

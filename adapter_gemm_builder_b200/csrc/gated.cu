@@ -25,6 +25,13 @@
 // Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
 // are sorted by adapter has few adapters per tile.
 //
+// More than 128 tokens usually run on pairs of CTAs (cta_group::2, clusters of two): 256 tokens by
+// the same columns, each CTA with its 128 rows of A and half of B (forward: the even CTA the
+// gate's rows, the odd one up's), so a stage is 32 KB instead of 48 and six of them cover the
+// latency of the loads, which had bounded the products (2048 x 8192 x 11008 without adapters:
+// three stages 590 us, four 544, five 506). The even CTA issues the MMAs; loads, LoRA
+// steps and drains run in both.
+//
 // Roles (576 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
 // chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..17 build
 // the LoRA steps. Two accumulators (512 TMEM columns), so a tile drains under the next one's
@@ -33,6 +40,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "act8.cuh"
 #include "internal.h"
@@ -54,15 +63,16 @@ constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the on
 constexpr int kGSmemShort = 192 * 1024;       // the same with fewer than 128 tokens
 constexpr int kGBarBytes = 512;
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
-constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);
+constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);  // rank blocks of 128 tokens
 enum { kGFwd = 0, kGBwd = 1 };
 // status bits of the bounded waits
 enum { kGStRing = 0x1, kGStMma = 0x2, kGStBuild = 0x4, kGStDrain = 0x8, kGStStall = 0x10 };
 
 struct GatedParams {
     int M, NC;        // tokens; output columns (F forward, K backward)
-    int mt, tiles;    // token tiles, all tiles
+    int mt, tiles;    // token tiles (of 128, or 256 for a pair), all tiles
     int bn, cols;     // accumulator columns of a tile; output columns of a tile (bn / 2 forward)
+    int b_bytes;      // a CTA's part of B in a stage
     int kb, kb_half;  // ring stages of a tile's main sum; backward: those of dg
     int stages, stage_bytes, a_bytes;
     int smem;         // dynamic shared memory
@@ -75,7 +85,7 @@ struct GatedParams {
     // LoRA
     const uint16_t* ops;      // [2][M][hi r16 | lo r16]: s_a v as bf16 halves
     const uint16_t* B;        // forward B [2][n_adapters][r_max][NC], backward A [2][n_adapters][NC][r_max]
-    const int32_t* lists;     // [mt][kListMax] rank blocks of a token tile (see block_code)
+    const int32_t* lists;     // [mt][kListMax per 128 tokens] rank blocks of a token tile (see block_code)
     const int32_t* list_len;  // [mt]
     const int32_t* tok_adapter;
     int n_adapters, r_max, r16;
@@ -96,10 +106,10 @@ __device__ __forceinline__ uint64_t g_desc_mn(uint32_t a, uint32_t atom)
     return (uint64_t)((a >> 4) & 0x3FFFu) | ((uint64_t)((atom >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// kind::f16, bf16 operands, fp32 accumulator, M = 128, N = n; B MN-major or K-major.
-__device__ __forceinline__ uint32_t g_idesc(int n, bool b_mn)
+// kind::f16, bf16 operands, fp32 accumulator, M = m, N = n; B MN-major or K-major.
+__device__ __forceinline__ uint32_t g_idesc(int m, int n, bool b_mn)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Bounded wait by one thread that sleeps between its probes.
@@ -183,8 +193,8 @@ __device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
 __device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
 __device__ __forceinline__ int block_live(int u) { return u & 63; }
 constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
-// The main stage after which the LoRA steps of a CTA's tile begin to be spread.
-__device__ __forceinline__ int lora_first(const GatedParams& p, int t) { return t == (int)blockIdx.x ? p.kb / 2 : 0; }
+// The main stage after which the LoRA steps of a tile begin to be spread (tile0: a CTA's first).
+__device__ __forceinline__ int lora_first(const GatedParams& p, int t, int tile0) { return t == tile0 ? p.kb / 2 : 0; }
 // LoRA steps of a token tile with this many rank blocks, both slices.
 __device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
 // Where a step's B part begins: behind the operand's tiles of 64 columns (four groups of 16:
@@ -197,7 +207,7 @@ __device__ __forceinline__ uint64_t g_desc_k64(uint32_t a)
            ((uint64_t)4 << 61);
 }
 
-template <int MODE, bool LORA>
+template <int MODE, bool LORA, bool PAIR>
 __global__ void __launch_bounds__(kGThreads, 1)
 gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                   const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GatedParams p)
@@ -205,6 +215,10 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader
+    constexpr int kCtas = PAIR ? 2 : 1, kTokens = kCtas * kGTileM;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
+    const int tile0 = (int)blockIdx.x / kCtas, tile_step = (int)gridDim.x / kCtas;
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t raw_u = ptx::smem_u32(smem_raw);
     const uint32_t base_u = (raw_u + 1023u) & ~1023u;
@@ -227,18 +241,25 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&lfull[b], 1);
+            ptx::mbar_init(&lfull[b], kCtas);
             ptx::mbar_init(&lempty[b], 1);
             ptx::mbar_init(&tfull[b], 1);
-            ptx::mbar_init(&tempty[b], kGDrainWarps);
+            ptx::mbar_init(&tempty[b], kCtas * kGDrainWarps);
         }
         ptx::mbar_init(mdone, 1);
         ptx::mbar_init(stall, 1);
         ptx::fence_mbar_init();
     }
+    __syncwarp();
+    if (PAIR) ptx::cluster_sync();  // the other CTA runs, its barriers are set up
     if (warp == kGMma) {
-        ptx::tmem_alloc(&s_tmem, 2 * kGAccCols);
-        ptx::tmem_relinquish();
+        if (PAIR) {
+            ptx::tmem_alloc2(&s_tmem, 2 * kGAccCols);
+            ptx::tmem_relinquish2();
+        } else {
+            ptx::tmem_alloc(&s_tmem, 2 * kGAccCols);
+            ptx::tmem_relinquish();
+        }
     }
     // Without adapters the operands may come from the kernel before this one. With them that
     // kernel is operand_kernel, and the one before it the shrink, which let operand_kernel (and so
@@ -250,6 +271,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_tmem;
+    // the leader's barriers that both CTAs signal (shared::cluster addresses)
+    auto leaders = [&](uint64_t* bar) { return PAIR ? ptx::mapa(ptx::smem_u32(bar), 0) : ptx::smem_u32(bar); };
 
     if (warp == kGProducer) {
         // ================================================================ producer
@@ -268,30 +291,42 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     ++use;
                 }
             };
-            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-                const int m = t % p.mt, n0 = (t / p.mt) * p.cols;
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+                if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
+                else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
+            };
+            for (int t = tile0; t < p.tiles && ok; t += tile_step) {
+                const int row0 = (t % p.mt) * kTokens + rank * kGTileM, n0 = (t / p.mt) * p.cols;
                 for (int kb = 0; kb < p.kb; ++kb) {
                     if (!(ok = acquire())) break;
                     const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
-                    ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(p.a_bytes + p.bn * 128));
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(kCtas * (p.a_bytes + p.b_bytes)));
                     if (MODE == kGFwd) {
-                        ptx::tma_load_2d(sa, &tmA0, &full[st], kb * kGKBlock, m * kGTileM);
-                        ptx::tma_load_2d(sb, &tmB0, &full[st], kb * kGKBlock, n0);
-                        ptx::tma_load_2d(sb + (uint32_t)(p.cols * 128), &tmB1, &full[st], kb * kGKBlock, n0);
+                        load(sa, &tmA0, kb * kGKBlock, row0);
+                        if (PAIR) {
+                            load(sb, rank ? &tmB1 : &tmB0, kb * kGKBlock, n0);
+                        } else {
+                            load(sb, &tmB0, kb * kGKBlock, n0);
+                            load(sb + (uint32_t)(p.cols * 128), &tmB1, kb * kGKBlock, n0);
+                        }
                     } else {
                         const bool up = kb >= p.kb_half;
-                        const int f0 = (up ? kb - p.kb_half : kb) * kGKBlock;
-                        ptx::tma_load_2d(sa, up ? &tmA1 : &tmA0, &full[st], f0, m * kGTileM);
-                        for (int b = 0; b < p.bn / 64; ++b)
-                            ptx::tma_load_2d(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, &full[st], n0 + b * 64, f0);
+                        const int f0 = (up ? kb - p.kb_half : kb) * kGKBlock, c0 = n0 + rank * (p.bn / 2);
+                        load(sa, up ? &tmA1 : &tmA0, f0, row0);
+                        for (int b = 0; b < p.b_bytes / 8192; ++b)
+                            load(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, c0 + b * 64, f0);
                     }
                     next();
                 }
             }
-            // every copy this CTA issued lands before it leaves: the last fill of each stage
-            for (int s = 0; s < p.stages; ++s) {
-                const uint32_t fills = use + (s < st ? 1 : 0);
-                if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
+            if (PAIR) {  // landed below, once both producers have stopped
+                for (int s = 0; s < p.stages; ++s) s_fills[s] = use + (s < st ? 1 : 0);
+            } else {
+                // every copy this CTA issued lands before it leaves: the last fill of each stage
+                for (int s = 0; s < p.stages; ++s) {
+                    const uint32_t fills = use + (s < st ? 1 : 0);
+                    if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
+                }
             }
         }
     } else if (warp == kGMma) {
@@ -303,7 +338,15 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         int st = 0, acc = 0;
         uint32_t use = 0, step = 0;  // turns of the ring; LoRA steps so far
         bool ok = true, waited = false;
-        const uint32_t id_main = g_idesc(p.bn, MODE == kGBwd), id_lora = g_idesc(p.cols, MODE == kGFwd);
+        const uint32_t id_main = g_idesc(kTokens, p.bn, MODE == kGBwd), id_lora = g_idesc(kTokens, p.cols, MODE == kGFwd);
+        auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
+            if (PAIR) ptx::tc_mma2_f16(d, a, b, id, more);
+            else ptx::tc_mma_f16_all(d, a, b, id, more);
+        };
+        auto commit = [](uint64_t* bar) {
+            if (PAIR) ptx::tc_commit2(bar);
+            else ptx::tc_commit(bar);
+        };
         // descriptors of stage 0 and of LoRA buffer 0; the address field counts 16-byte units
         const uint32_t lora_u = base_u + (uint32_t)(p.stages * p.stage_bytes), lora_bu = lora_u + lora_b_offset(p);
         const uint64_t da0 = g_desc_k(base_u);
@@ -311,9 +354,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         const uint64_t la0 = g_desc_k(lora_u);
         const uint64_t lb0 = MODE == kGFwd ? g_desc_mn(lora_bu, (uint32_t)(p.ups * 2048)) : g_desc_k64(lora_bu);
         const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++acc) {
+        for (int t = rank == 0 ? tile0 : p.tiles; t < p.tiles && ok; t += tile_step, ++acc) {
             const int m = t % p.mt, buf = acc & 1;
-            const int first = lora_first(p, t), spread = p.kb - first;
+            const int first = lora_first(p, t, tile0), spread = p.kb - first;
             int blocks = LORA && waited ? p.list_len[m] : 0;
             if (acc >= 2 && !(ok = wait_warp(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
                                              p.timeout_ns)))
@@ -328,8 +371,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         const uint64_t da = da0 + (uint32_t)st * stage16, db = db0 + (uint32_t)st * stage16;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            ptx::tc_mma_f16_all(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, (kb | ks) ? 1u : 0u);
-                        ptx::tc_commit(&empty[st]);
+                            mma(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, (kb | ks) ? 1u : 0u);
+                        commit(&empty[st]);
                     }
                     __syncwarp();
                     if (++st == p.stages) {
@@ -364,10 +407,10 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             for (int h = 0; h < 2; ++h)
                                 for (int k = 0; k < n; ++k) {
                                     const int c = h * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
-                                    ptx::tc_mma_f16_all(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
+                                    mma(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
                                                     lb0 + at + (uint32_t)(k * (MODE == kGFwd ? 128 : 2)), id_lora, 1u);
                                 }
-                            ptx::tc_commit(&lempty[lb]);
+                            commit(&lempty[lb]);
                         }
                         __syncwarp();
                     }
@@ -378,13 +421,15 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     due += n * ext;
                 }
             }
-            if (ok && leader) ptx::tc_commit(&tfull[buf]);
+            if (ok && leader) commit(&tfull[buf]);
             __syncwarp();
         }
-        // every MMA issued is complete before the CTA leaves
-        if (leader) ptx::tc_commit(mdone);
-        __syncwarp();
-        wait_warp(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns, false);
+        // every MMA issued is complete before the CTA (of a pair: either, by the barrier below) leaves
+        if (rank == 0) {
+            if (leader) commit(mdone);
+            __syncwarp();
+            wait_warp(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns, false);
+        }
     } else if (warp >= kGBuilder0) {
         // ================================================================ LoRA steps
         if (LORA) {
@@ -392,13 +437,14 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             const int bt = threadIdx.x - kGBuilder0 * 32;
             // A builder's pieces lie in one column of 16-byte pieces, a fixed number of rows apart
             // (a multiple of eight, so their swizzle is the same): piece i of the operand in row
-            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c. Forward, a pass of
-            // B's rows is one rank block (b_step 16).
+            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c (forward a row is
+            // a rank, 16 to a block; backward an output column).
             const int a_lg = p.ups == 4 ? 4 : 3, a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
             const int a_rows = p.a_bytes >> 7;
             const int a_half = a_c >> (a_lg - 1), a_k = a_c & ((1 << (a_lg - 1)) - 1);  // hi or lo; piece of the blocks
-            const int b_lg = MODE == kGFwd ? 4 : 2, b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
-            const int b_rows = MODE == kGFwd ? (b_c < p.cols >> 3 ? 16 * p.ups : 0) : p.cols;
+            const int b_lg = MODE == kGFwd ? (PAIR ? 3 : 4) : 2, b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
+            const int b_cols = p.cols / kCtas, b_n0 = rank * b_cols;  // this CTA's columns of the tile
+            const int b_rows = MODE == kGFwd ? (b_c < b_cols >> 3 ? 16 * p.ups : 0) : b_cols;
             const uint32_t a_off = (uint32_t)((a_c >> 3) * p.a_bytes + a_row * 128 + (((a_c & 7) ^ (a_row & 7)) << 4));
             const uint32_t b_off =
                 lora_b_offset(p) + (MODE == kGFwd ? (uint32_t)((b_c >> 3) * (p.ups * 2048) + b_row * 128 + (((b_c & 7) ^ (b_row & 7)) << 4))
@@ -406,22 +452,23 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             uint8_t* bufs = ring + p.stages * p.stage_bytes;
 
             // the walk over the steps: tile t, its step e of `ext`
-            int t = blockIdx.x, e = -1, ext = 0, m = 0, n0 = 0, blocks = 0;
+            int t = tile0, e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;
             bool open = false;
             int ids[kGMaxA];  // adapters of this builder's operand rows
             auto advance = [&]() -> bool {
-                for (;; t += gridDim.x, open = false) {
+                for (;; t += tile_step, open = false) {
                     if (t >= p.tiles) return false;
                     if (!open) {
                         m = t % p.mt;
-                        n0 = (t / p.mt) * p.cols;
+                        n0 = (t / p.mt) * p.cols + b_n0;
+                        row0 = m * kTokens + rank * kGTileM;
                         blocks = p.list_len[m];
                         ext = lora_steps(p, blocks);
                         e = -1;
                         open = true;
 #pragma unroll
                         for (int i = 0; i < kGMaxA; ++i) {
-                            const int row = a_row + i * a_step, tok = m * kGTileM + row;
+                            const int row = a_row + i * a_step, tok = row0 + row;
                             ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
                         }
                     }
@@ -432,13 +479,13 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             int ua, ub[kGMaxB];
             auto blocks_of_step = [&]() {
                 const int b0 = (e >> 1) * p.ups;
-                const int32_t* list = p.lists + (size_t)m * kListMax;
+                const int32_t* list = p.lists + (size_t)m * kListMax * kCtas;
                 const int ka = b0 + (a_k >> 1);
                 ua = ka < blocks ? list[ka] : kNoBlock;
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i) {
-                    const int kb = b0 + (MODE == kGFwd ? i : b_c >> 1);
-                    ub[i] = (MODE == kGFwd ? i < p.ups : i == 0) && kb < blocks ? list[kb] : kNoBlock;
+                    const int kk = MODE == kGFwd ? (b_row + i * b_step) >> 4 : b_c >> 1, kb = b0 + kk;
+                    ub[i] = (MODE == kGFwd || i == 0) && kk < p.ups && kb < blocks ? list[kb] : kNoBlock;
                 }
             };
             uint4 ra[kGMaxA], rb[kGMaxB];
@@ -449,7 +496,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                 for (int i = 0; i < kGMaxA; ++i) {
                     ra[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (ids[i] == block_adapter(ua))
-                        ra[i] = *reinterpret_cast<const uint4*>(src + (size_t)(m * kGTileM + a_row + i * a_step) * (2 * p.r16));
+                        ra[i] = *reinterpret_cast<const uint4*>(src + (size_t)(row0 + a_row + i * a_step) * (2 * p.r16));
                 }
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i) {
@@ -457,8 +504,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     rb[i] = make_uint4(0u, 0u, 0u, 0u);
                     const size_t pool = ((size_t)s * p.n_adapters + block_adapter(u)) * p.r_max * p.NC;
                     if (MODE == kGFwd) {  // a row of B_a, eight columns
-                        if (row < b_rows && b_row < block_live(u) && n0 + b_c * 8 < p.NC)
-                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(block_rank0(u) + b_row) * p.NC + n0 + b_c * 8);
+                        const int j = row & 15;
+                        if (row < b_rows && j < block_live(u) && n0 + b_c * 8 < p.NC)
+                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(block_rank0(u) + j) * p.NC + n0 + b_c * 8);
                     } else {  // a row of A_a, eight ranks
                         const int j = (b_c & 1) * 8;
                         if (row < b_rows && j < block_live(u) && n0 + row < p.NC)
@@ -496,22 +544,25 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                 ptx::fence_proxy_async_smem();
                 if (more) load();  // in flight over the barrier and the next wait
                 ptx::named_sync(2, kGBuilders);
-                if (bt == 0) ptx::mbar_arrive(&lfull[lb]);
+                if (bt == 0) {
+                    if (PAIR) ptx::mbar_arrive_remote(leaders(&lfull[lb]));
+                    else ptx::mbar_arrive(&lfull[lb]);
+                }
             }
         }
     } else {
         // ================================================================ drain
         const int q = warp & 3, half = warp >> 2;
         int acc = 0;
-        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++acc) {
-            const int m = t % p.mt, n0 = (t / p.mt) * p.cols, buf = acc & 1;
-            const int row = m * kGTileM + q * 32 + lane;
+        for (int t = tile0; t < p.tiles; t += tile_step, ++acc) {
+            const int row0 = (t % p.mt) * kTokens + rank * kGTileM + q * 32, n0 = (t / p.mt) * p.cols, buf = acc & 1;
+            const int row = row0 + lane;
             if (!wait_role(3, kGDrainWarps * 32, threadIdx.x == 0, &tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status,
                            kGStDrain, p.timeout_ns))
                 break;
             ptx::tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGAccCols);
-            if (m * kGTileM + q * 32 < p.M) {  // the warp has live rows
+            if (row0 < p.M) {  // the warp has live rows
                 if (MODE == kGFwd && p.g_codes) {
                     const int nb = (p.NC + act8::kBlock - 1) / act8::kBlock;
                     for (int c = half * 32; c < p.cols; c += 64) {
@@ -553,15 +604,38 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_remote(leaders(&tempty[buf]));
+                else ptx::mbar_arrive(&tempty[buf]);
+            }
         }
     }
 
     ptx::tc_fence_before();
-    __syncthreads();
+    if (PAIR) {
+        // Both CTAs' roles are done and no more copies are issued. Every copy counts on the leader's
+        // barriers: it sees each stage's last fill through before either CTA leaves. After an
+        // abort the two producers may differ by one fill; the missing side's bytes are counted
+        // here then.
+        __syncwarp();
+        ptx::cluster_sync();
+        if (rank == 0 && threadIdx.x < p.stages) {
+            const int s = (int)threadIdx.x;
+            const uint32_t mine = s_fills[s], other = ptx::ld_dsmem_u32(ptx::mapa(ptx::smem_u32(&s_fills[s]), 1));
+            const uint32_t half = (uint32_t)(p.a_bytes + p.b_bytes), fills = mine > other ? mine : other;
+            if (mine > other) ptx::mbar_complete_tx(&full[s], half);
+            if (mine < other) ptx::mbar_arrive_expect_tx(&full[s], half);
+            if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
+        }
+        __syncwarp();
+        ptx::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == kGMma) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 2 * kGAccCols);
+        if (PAIR) ptx::tmem_dealloc2(tmem, 2 * kGAccCols);
+        else ptx::tmem_dealloc(tmem, 2 * kGAccCols);
     }
 }
 
@@ -575,13 +649,14 @@ struct OperandParams {
     const int32_t* ranks;
     const float* scales;
     int M, n_adapters, r_max, r16;
+    int tile;  // tokens a list covers: 128 or 256
     uint16_t* ops;
     int32_t* lists;
     int32_t* list_len;
 };
 
-constexpr int kOpThreads = 128;
-constexpr int kOpCtas = 8;  // CTAs per token tile, 16 rows each
+constexpr int kOpThreads = 256;
+constexpr int kOpRows = 16;  // tokens per CTA
 
 // s_a v of both slices as bf16 halves hi + lo (columns past the rank zero), and per token tile the rank blocks that its rows use, adapters in order of first appearance.
 // Lets the GEMM start at once (see the wait there).
@@ -590,12 +665,11 @@ operand_kernel(const OperandParams p)
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kRows = kGTileM / kOpCtas;
-    const int chunks = p.r16 >> 3, items = 2 * kRows * chunks;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunks = p.r16 >> 3, items = 2 * kOpRows * chunks;
     for (int i = tid; i < items; i += kOpThreads) {
-        const int c = i % chunks, rs = i / chunks, s = rs / kRows;
-        const int row = m * kGTileM + (int)blockIdx.y * kRows + rs % kRows;
+        const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
+        const int row = (int)blockIdx.x * kOpRows + rs % kOpRows;
         if (row >= p.M) continue;
         const int a = p.tok_adapter[row];
         if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
@@ -626,11 +700,12 @@ operand_kernel(const OperandParams p)
             o[part * chunks + c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    if (blockIdx.y != 0) return;
-    __shared__ int s_id[kGTileM];
-    __shared__ int s_cnt[kGTileM / 32];
-    const int row = m * kGTileM + tid;
-    int id = row < p.M ? p.tok_adapter[row] : -1;
+    const int per = p.tile / kOpRows, m = (int)blockIdx.x / per;
+    if ((int)blockIdx.x % per) return;  // one CTA of the tile makes its list
+    __shared__ int s_id[kOpThreads];
+    __shared__ int s_cnt[kOpThreads / 32];
+    const int row = m * p.tile + tid;
+    int id = tid < p.tile && row < p.M ? p.tok_adapter[row] : -1;
     if (id >= p.n_adapters) id = -1;
     s_id[tid] = id;
     __syncthreads();
@@ -648,39 +723,19 @@ operand_kernel(const OperandParams p)
     __syncthreads();
     int total = 0;
     at -= mine;
-    for (int w = 0; w < kGTileM / 32; ++w) {
+    for (int w = 0; w < kOpThreads / 32; ++w) {
         if (w < warp) at += s_cnt[w];
         total += s_cnt[w];
     }
-    for (int b = 0; b < mine; ++b) p.lists[(size_t)m * kListMax + at + b] = block_code(id, b, min(16, rank - 16 * b));
+    int32_t* list = p.lists + (size_t)m * kListMax * (p.tile / kGTileM);
+    for (int b = 0; b < mine; ++b) list[at + b] = block_code(id, b, min(16, rank - 16 * b));
     if (tid == 0) p.list_len[m] = total;
 }
 
-// The columns of a tile: the smallest of rounds x columns (rounds of the grid over the SMs) with
-// a penalty on narrow tiles, whose stages carry fewer weight bytes per turn of the ring and read
-// their operands from shared memory more often per product. A single round has no such choice
-// to make: there narrower tiles only bring in more SMs. (8192 x 28672, 16 tokens: 112
-// columns in two rounds 6.1 TB/s of weights, 16 columns in thirteen 1.9 TB/s.)
-int tile_cols(int NC, int mt, int sms, const int* choices, int n_choices, const float* cost)
-{
-    int best = choices[0];
-    double least = 0;
-    for (int i = 0; i < n_choices; ++i) {
-        const long long tiles = (long long)mt * ((NC + choices[i] - 1) / choices[i]);
-        const long long rounds = (tiles + sms - 1) / sms;
-        const double v = (double)rounds * choices[i] * (rounds > 1 || mt > 1 ? cost[i] : 1.f);
-        if (i == 0 || v < least) {
-            least = v;
-            best = choices[i];
-        }
-    }
-    return best;
-}
-
-template <int MODE, bool LORA>
+template <int MODE, bool LORA, bool PAIR>
 cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int grid, cudaStream_t stream)
 {
-    auto kern = gated_gemm_kernel<MODE, LORA>;
+    auto kern = gated_gemm_kernel<MODE, LORA, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -688,12 +743,88 @@ cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int gr
     cfg.blockDim = dim3(kGThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)p.smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+}
+
+// Pairs of CTAs that the current device runs at once (an SM without a partner stays idle).
+int pair_count()
+{
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n) return n > 0 ? n : 0;
+    auto kern = gated_gemm_kernel<kGFwd, true, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2), 1, 1);
+    cfg.blockDim = dim3(kGThreads, 1, 1);
+    cfg.dynamicSmemBytes = kGSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+        n = -1;
+    cached[dev].store(n, std::memory_order_relaxed);
+    return n > 0 ? n : 0;
+}
+
+struct GatedPlan {
+    bool pair;
+    int cols, mt, tiles, grid;
+};
+
+// The tiles of a call: the smallest of rounds x columns (rounds of the CTAs or pairs that run at
+// once) with a penalty on narrow tiles, whose stages carry fewer bytes per turn of the ring
+// and read their operands from shared memory more often per product; where one round holds all
+// tiles of a single token tile, narrower ones only bring in more SMs. (8192 x 28672, 16 tokens:
+// 112 columns in two rounds 6.1 TB/s of weights, 16 columns in thirteen 1.9 TB/s.) Single CTAs pay
+// an eighth for their shallower ring, so pairs take every call whose tiles fill them.
+GatedPlan gated_plan(bool bwd, int M, int NC, bool save)
+{
+    // output columns; forward with checkpoints: whole blocks of 32, and for pairs the adapters'
+    // MMA of half the columns wants 32 too
+    static const int fwd[] = {128, 96, 64, 32, 112, 80, 48, 16}, back[] = {256, 192, 128, 64};
+    static const double fwd_cost[] = {1, 1.04, 1.15, 1.8, 1.02, 1.08, 1.4, 3}, back_cost[] = {1, 1.04, 1.15, 1.8};
+    static const int fwd2[] = {128, 96, 64}, back2[] = {256, 128};
+    static const double fwd2_cost[] = {1, 1.04, 1.15}, back2_cost[] = {1, 1.15};
+    GatedPlan best = {};
+    double least = 0;
+    auto consider = [&](bool pair, const int* cols, const double* cost, int n, int units) {
+        const int mt = (M + (pair ? 255 : 127)) / (pair ? 256 : 128);
+        for (int i = 0; i < n; ++i) {
+            const long long tiles = (long long)mt * ((NC + cols[i] - 1) / cols[i]), rounds = (tiles + units - 1) / units;
+            const double v = (double)rounds * cols[i] * (rounds > 1 || mt > 1 || pair ? cost[i] : 1) * (pair ? 1 : 1.125);
+            if (best.cols && v >= least) continue;
+            least = v;
+            best.pair = pair;
+            best.cols = cols[i];
+            best.mt = mt;
+            best.tiles = (int)tiles;
+            best.grid = (int)(tiles < units ? tiles : units) * (pair ? 2 : 1);
+        }
+    };
+    if (bwd) consider(false, back, back_cost, 4, device_sm_count());
+    else consider(false, fwd, fwd_cost, save ? 4 : 8, device_sm_count());
+    const int pairs = M > kGTileM ? pair_count() : 0;
+    if (pairs) {
+        if (bwd) consider(true, back2, back2_cost, 2, pairs);
+        else consider(true, fwd2, fwd2_cost, 3, pairs);
+    }
+    return best;
 }
 
 }  // namespace
@@ -705,15 +836,15 @@ size_t gated_operand_bytes(int M, int r_max)
 }
 size_t gated_list_bytes(int M)
 {
-    const size_t mt = (size_t)(M + kGTileM - 1) / kGTileM;
-    return mt * (kListMax + 1) * 4;
+    return (size_t)(M + 2 * kGTileM - 1) / (2 * kGTileM) * 2 * (kListMax + 1) * 4;
 }
 
 cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
-                                  void* ops, void* lists, cudaStream_t stream)
+                                  bool backward, bool save, void* ops, void* lists, cudaStream_t stream)
 {
-    const int mt = (M + kGTileM - 1) / kGTileM;
+    const GatedPlan plan = gated_plan(backward, M, backward ? pool.h_in : pool.h_out, save);
     OperandParams p = {};
+    p.tile = plan.pair ? 2 * kGTileM : kGTileM;
     p.v = v;
     p.planes = planes;
     p.plane = (long long)pool.n_slices * M * pool.r_max;
@@ -726,9 +857,9 @@ cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t&
     p.r16 = (pool.r_max + 15) / 16 * 16;
     p.ops = static_cast<uint16_t*>(ops);
     p.lists = static_cast<int32_t*>(lists);
-    p.list_len = p.lists + (size_t)mt * kListMax;
+    p.list_len = p.lists + (size_t)plan.mt * kListMax * (p.tile / kGTileM);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)mt, kOpCtas, 1);
+    cfg.gridDim = dim3((unsigned)(plan.mt * (p.tile / kOpRows)), 1, 1);
     cfg.blockDim = dim3(kOpThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -745,21 +876,12 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     GatedParams p = {};
     p.M = a.M;
     p.NC = bwd ? a.K : a.F;
-    p.mt = (a.M + kGTileM - 1) / kGTileM;
-    const int sms = device_sm_count();
     const bool save = a.g8 != nullptr;
-    if (bwd) {
-        static const int c[] = {256, 192, 128, 64};
-        static const float cost[] = {1.f, 1.04f, 1.15f, 1.8f};
-        p.cols = tile_cols(p.NC, p.mt, sms, c, 4, cost);
-        p.bn = p.cols;
-    } else {
-        static const int c[] = {128, 96, 64, 32, 112, 80, 48, 16};  // checkpoint blocks: multiples of 32
-        static const float cost[] = {1.f, 1.04f, 1.15f, 1.8f, 1.02f, 1.08f, 1.4f, 3.f};
-        p.cols = tile_cols(p.NC, p.mt, sms, c, save ? 4 : 8, cost);
-        p.bn = 2 * p.cols;
-    }
-    p.tiles = p.mt * ((p.NC + p.cols - 1) / p.cols);
+    const GatedPlan plan = gated_plan(bwd, a.M, p.NC, save);
+    p.mt = plan.mt;
+    p.cols = plan.cols;
+    p.bn = bwd ? p.cols : 2 * p.cols;
+    p.tiles = plan.tiles;
     const int red = bwd ? a.F : a.K;
     p.kb_half = (red + kGKBlock - 1) / kGKBlock;
     p.kb = bwd ? 2 * p.kb_half : p.kb_half;
@@ -767,7 +889,8 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     // the shared memory holds and land in accumulator rows that nobody drains
     const int a_rows = a.M >= kGTileM ? kGTileM : (a.M + 7) / 8 * 8;
     p.a_bytes = a_rows * 128;
-    p.stage_bytes = p.a_bytes + p.bn * 128;
+    p.b_bytes = p.bn * 128 / (plan.pair ? 2 : 1);
+    p.stage_bytes = p.a_bytes + p.b_bytes;
     // Full token tiles take all shared memory. Fewer tokens leave some of it, so that the small
     // kernels before this one keep running beside its CTAs (which then start at once, the
     // weights streaming under the shrink); their 16 KB at the end are what the MMA may read past a
@@ -778,7 +901,8 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.r16 = (a.r_max + 15) / 16 * 16;
         // rank blocks per step: what four pieces per builder and the space beside four stages hold
         p.ups = !bwd && a_rows <= 64 ? 4 : 2;
-        p.lora_bytes = (int)lora_b_offset(p) + (bwd ? p.cols * 64 : (p.cols + 63) / 64 * p.ups * 2048);
+        const int half = p.cols / (plan.pair ? 2 : 1);
+        p.lora_bytes = (int)lora_b_offset(p) + (bwd ? half * 64 : (half + 63) / 64 * p.ups * 2048);
         p.lora_bytes = (p.lora_bytes + 1023) / 1024 * 1024;
         p.lbufs = room - 2 * p.lora_bytes >= 4 * p.stage_bytes ? 2 : 1;
         room -= p.lbufs * p.lora_bytes;
@@ -800,7 +924,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.ops = static_cast<const uint16_t*>(a.ops);
         p.B = static_cast<const uint16_t*>(a.B);
         p.lists = static_cast<const int32_t*>(a.lists);
-        p.list_len = p.lists + (size_t)p.mt * kListMax;
+        p.list_len = p.lists + (size_t)p.mt * kListMax * (plan.pair ? 2 : 1);
         p.tok_adapter = a.tok_adapter;
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
@@ -816,10 +940,12 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
                                   bwd ? kGKBlock : (uint32_t)p.cols, sw);
     }
     if (!ok) return cudaErrorInvalidValue;
-    const int grid = p.tiles < sms ? p.tiles : sms;
-    if (bwd)
-        return a.lora ? launch_mode<kGBwd, true>(tm, p, grid, stream) : launch_mode<kGBwd, false>(tm, p, grid, stream);
-    return a.lora ? launch_mode<kGFwd, true>(tm, p, grid, stream) : launch_mode<kGFwd, false>(tm, p, grid, stream);
+    if (plan.pair) {
+        if (bwd) return a.lora ? launch_mode<kGBwd, true, true>(tm, p, plan.grid, stream) : launch_mode<kGBwd, false, true>(tm, p, plan.grid, stream);
+        return a.lora ? launch_mode<kGFwd, true, true>(tm, p, plan.grid, stream) : launch_mode<kGFwd, false, true>(tm, p, plan.grid, stream);
+    }
+    if (bwd) return a.lora ? launch_mode<kGBwd, true, false>(tm, p, plan.grid, stream) : launch_mode<kGBwd, false, false>(tm, p, plan.grid, stream);
+    return a.lora ? launch_mode<kGFwd, true, false>(tm, p, plan.grid, stream) : launch_mode<kGFwd, false, false>(tm, p, plan.grid, stream);
 }
 
 }  // namespace lora

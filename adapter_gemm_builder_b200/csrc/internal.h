@@ -72,7 +72,8 @@ cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cud
 
 // The gated feed-forward block. launch_gated_operands turns `planes` planes of v
 // [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
-// lists the rank blocks of each 128-token tile (gated_list_bytes). With adapters the launches
+// lists the rank blocks of each token tile of the GEMM that follows (backward or not, saving
+// checkpoints or not; gated_list_bytes). With adapters the launches
 // right before launch_gated_gemm are a shrink that waits for its predecessors before it lets
 // its dependents start, then launch_gated_operands (gated.cu says why).
 // launch_gated_shrink: `planes` (gated_shrink_planes) planes of v[s][t][j] = sum_l lng[s][t][l] w,
@@ -84,7 +85,7 @@ cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, i
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
 cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
-                                  void* ops, void* lists, cudaStream_t stream);
+                                  bool backward, bool save, void* ops, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
     bool backward;
     int M, K, F, act;

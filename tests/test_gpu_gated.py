@@ -123,6 +123,9 @@ FORWARD = [
     (127, 200, 136, 5, 32, "zipf"), (128, 64, 128, 1, 64, "uniform"), (129, 1024, 392, 4, 64, "zipf"),
     (300, 128, 4096, 3, 16, "sorted_zipf"), (257, 328, 2064, 130, 8, "uniform"), (640, 192, 24, 2, 32, "sorted_zipf"),
     (1025, 96, 520, 7, 64, "zipf"),
+    # wide enough for pairs of CTAs: whole and ragged pairs, the odd CTA without tokens, many adapters
+    (512, 128, 9600, 0, 8, "uniform"), (700, 136, 9496, 3, 16, "sorted_zipf"), (1100, 64, 5000, 300, 8, "uniform"),
+    (2049, 72, 3000, 9, 64, "zipf"),
 ]
 
 
@@ -135,7 +138,7 @@ def test_forward(M, K, F, n, r, ids, act):
 
 @pytest.mark.parametrize("M,K,F,n,r,ids", [(1, 64, 16, 0, 8, "uniform"), (5, 128, 48, 2, 8, "uniform"),
                                            (130, 256, 1040, 5, 16, "zipf"), (513, 200, 272, 3, 64, "sorted_zipf"),
-                                           (256, 64, 4112, 2, 32, "identical")])
+                                           (256, 64, 4112, 2, 32, "identical"), (600, 96, 9616, 4, 64, "sorted_zipf")])
 def test_forward_with_checkpoints(M, K, F, n, r, ids):
     """h as without them; a block's scale is the rule's for a largest element within the error of the
     sum, and an element is within half an E4M3 step (2^-4, or half the smallest step) of g or u."""
@@ -235,6 +238,9 @@ def check_backward(p, act, o):
     (64, 512, 256, 6, 32, "zipf", "gelu", True, True), (150, 200, 1040, 3, 64, "sorted_zipf", "silu", False, False),
     (333, 1040, 400, 5, 8, "zipf", "gelu", False, True), (128, 256, 128, 0, 8, "uniform", "gelu", False, True),
     (1030, 336, 144, 4, 16, "sorted_zipf", "silu", True, False), (256, 640, 208, 2, 64, "identical", "silu", True, True),
+    # pairs of CTAs
+    (512, 9600, 80, 0, 8, "uniform", "silu", False, False), (900, 9576, 48, 5, 64, "sorted_zipf", "silu", False, True),
+    (1281, 5008, 112, 200, 8, "uniform", "gelu", True, False),
 ])
 def test_backward(M, K, F, n, r, ids, act, x8, h):
     p = Problem(M, K, F, n, r, ids)
