@@ -114,7 +114,7 @@ size_t bwd_ws_layout(int M, const lora_pool_t* pool, size_t* off_at, size_t* off
     return off;
 }
 
-// Gated forward workspace: status | planes of v | operands | adapter lists (adapters only).
+// Gated forward workspace: status | with adapters: planes of v | operands | rank blocks.
 struct GatedWs {
     size_t v, ops, lists, size;
 };
@@ -132,15 +132,17 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     return w;
 }
 
-// Gated backward workspace: status | dg, du | with adapters: x expanded | planes of u, then of
-// v | operands of u, of v | adapter lists.
+// Gated backward workspace: status | counts | parts of shared tiles | dg, du | with adapters:
+// x expanded | planes of u, then of v | operands of u, of v | rank blocks.
 struct GatedBwdWs {
-    size_t d, x, v, ops_u, ops_v, lists, size;
+    size_t count, part, d, x, v, ops_u, ops_v, lists, size;
 };
 GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 {
     GatedBwdWs w = {};
-    w.size = 256;
+    w.count = 256;
+    w.part = w.count + align256(gated_count_bytes());
+    w.size = w.part + align256(gated_part_bytes());
     w.d = w.size;
     w.size += align256((size_t)2 * M * F * 2);
     if (!pool) return w;
@@ -657,7 +659,8 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
-        if (gated_operands(true, g8 != nullptr, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists, s) != cudaSuccess)
+        if (gated_operands(true, g8 != nullptr, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists,
+                           s) != cudaSuccess)
             return LORA_ERR_CUDA;
         a.lora = true;
         a.ops = w + l.ops;
@@ -693,7 +696,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     uint16_t* dg = reinterpret_cast<uint16_t*>(w + l.d);
     uint16_t* du = dg + (size_t)M * F;
     // 1. dg, du (and h) from the checkpoints
-    if (launch_gated_point(dh, M, F, act, *g8, *u8, dg, du, h, s) != cudaSuccess) return LORA_ERR_CUDA;
+    int* count = reinterpret_cast<int*>(w + l.count);
+    if (launch_gated_point(dh, M, F, act, *g8, *u8, dg, du, h, count, s) != cudaSuccess) return LORA_ERR_CUDA;
     GatedGemmArgs a = {};
     a.backward = true;
     a.M = M;
@@ -705,6 +709,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.W[1] = Wu;
     a.out = dX;
     a.status = reinterpret_cast<uint32_t*>(w);
+    a.part = reinterpret_cast<float*>(w + l.part);
+    a.count = count;
     if (!pool) return cuda_status(launch_gated_gemm(a, s));
     // 2. u = d.B^T of both slices
     float* v = reinterpret_cast<float*>(w + l.v);

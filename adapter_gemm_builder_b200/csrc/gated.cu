@@ -32,6 +32,16 @@
 // three stages 590 us, four 544, five 506). The even CTA issues the MMAs; loads, LoRA
 // steps and drains run in both.
 //
+// The backward has few tiles where the tokens are few, with long sums: 16 tokens have 32 tiles for
+// 148 SMs. The tiles of its last round are then shared: their sums are cut into S pieces of
+// equal length, spread over all units; a piece writes its fp32 accumulator to the workspace, and
+// whichever piece of a tile is done last adds all of them in order and finishes the tile
+// (nobody waits for another, and the sum does not depend on who is last). Units that run side by
+// side take the same piece of neighbouring tiles, so they read the same weights at the same
+// time. (4096 x 11008: 16 tokens 119 -> 47 us, 512 tokens 156 -> 110 us; cutting the stages of all
+// shared tiles into one equal run per unit made 1024 tokens 212 us instead of 164, by reading the
+// weights at different times; in the forward, bound by power, sharing gained nothing.)
+//
 // Roles (576 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
 // chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..17 build
 // the LoRA steps. Two accumulators (512 TMEM columns), so a tile drains under the next one's
@@ -57,12 +67,13 @@ constexpr int kGBuilders = 256;
 constexpr int kGMaxA = 4, kGMaxB = 4;        // 16-byte pieces of a LoRA step per builder
 constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
 constexpr int kGTileM = 128;
-constexpr int kGMaxStages = 8;
+constexpr int kGMaxStages = 12;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
 constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
 constexpr int kGSmemShort = 192 * 1024;       // the same with fewer than 128 tokens
 constexpr int kGBarBytes = 512;
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
+constexpr int kGCounts = 256;                 // counts of shared tiles (fewer than units, two CTAs each)
 constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);  // rank blocks of 128 tokens
 enum { kGFwd = 0, kGBwd = 1 };
 // status bits of the bounded waits
@@ -76,6 +87,11 @@ struct GatedParams {
     int kb, kb_half;  // ring stages of a tile's main sum; backward: those of dg
     int stages, stage_bytes, a_bytes;
     int smem;         // dynamic shared memory
+    int units, rounds;    // CTAs or pairs; whole tiles of each: tile = unit + round * units
+    int whole, shared;    // tiles before the shared ones; shared tiles
+    int split;            // pieces of a shared tile
+    float* part;          // [shared][split][CTAs][bn / 4][128][4] accumulators of pieces
+    int* count;           // [shared][CTAs] pieces done, zero on entry (the element-wise kernel)
     int act;
     uint16_t* out;    // h [M][F] or dX [M][K]
     uint8_t *g_codes, *g_scales, *u_codes, *u_scales;  // forward checkpoints or NULL
@@ -187,14 +203,39 @@ __device__ __forceinline__ void save_block(const float* v, int n, uint8_t* codes
     *scale = (uint8_t)E;
 }
 
+// A unit's work, as every role walks it: stages [k0, k1) of a tile at a time.
+struct Walk {
+    int unit, round, tile, piece, k0, k1, seen;
+    __device__ explicit Walk(int u) : unit(u), round(0), seen(0) {}
+    __device__ __forceinline__ bool next(const GatedParams& p)
+    {
+        ++seen;
+        piece = -1;
+        k0 = 0;
+        k1 = p.kb;
+        if (round < p.rounds) {
+            tile = unit + round++ * p.units;
+            if (tile < p.tiles) return true;
+        }
+        const int q = unit + (round - p.rounds) * p.units;
+        if (q >= p.shared * p.split) return false;
+        ++round;
+        piece = q / p.shared;
+        tile = p.whole + q - piece * p.shared;
+        k0 = (int)((long long)p.kb * piece / p.split);
+        k1 = (int)((long long)p.kb * (piece + 1) / p.split);
+        return true;
+    }
+    // the stage after which the tile's LoRA steps begin to be spread: a unit's first piece leaves the
+    // shrink its first half
+    __device__ __forceinline__ int lora_first() const { return seen == 1 ? k0 + (k1 - k0) / 2 : k0; }
+};
 // A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has.
 __device__ __forceinline__ int block_code(int adapter, int block, int live) { return adapter << 8 | block << 6 | live; }
 __device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
 __device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
 __device__ __forceinline__ int block_live(int u) { return u & 63; }
 constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
-// The main stage after which the LoRA steps of a tile begin to be spread (tile0: a CTA's first).
-__device__ __forceinline__ int lora_first(const GatedParams& p, int t, int tile0) { return t == tile0 ? p.kb / 2 : 0; }
 // LoRA steps of a token tile with this many rank blocks, both slices.
 __device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
 // Where a step's B part begins: behind the operand's tiles of 64 columns (four groups of 16:
@@ -215,10 +256,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
+    __shared__ int s_last;       // this CTA's part of a shared tile was the last
     __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader
     constexpr int kCtas = PAIR ? 2 : 1, kTokens = kCtas * kGTileM;
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
-    const int tile0 = (int)blockIdx.x / kCtas, tile_step = (int)gridDim.x / kCtas;
+    const int unit = (int)blockIdx.x / kCtas;
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t raw_u = ptx::smem_u32(smem_raw);
     const uint32_t base_u = (raw_u + 1023u) & ~1023u;
@@ -276,30 +318,22 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 
     if (warp == kGProducer) {
         // ================================================================ producer
-        if (lane == 0) {
-            int st = 0;
-            uint32_t use = 0;            // uses of stage st before this one (all stages below st: one more)
-            bool ok = true;
-            if (p.inject_stall && blockIdx.x == 0)  // test hook: a wait that runs out
-                ok = wait_bar(stall, 0, abort_flag, status, kGStStall, p.timeout_ns);
-            auto acquire = [&]() {
-                return use == 0 || wait_bar(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
-            };
-            auto next = [&]() {
-                if (++st == p.stages) {
-                    st = 0;
-                    ++use;
-                }
-            };
-            auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
-                if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
-                else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
-            };
-            for (int t = tile0; t < p.tiles && ok; t += tile_step) {
-                const int row0 = (t % p.mt) * kTokens + rank * kGTileM, n0 = (t / p.mt) * p.cols;
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!(ok = acquire())) break;
-                    const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+        const bool leader = ptx::elect_one();
+        int st = 0;
+        uint32_t use = 0;  // uses of stage st before this one (of the stages below st: one more)
+        bool ok = true;
+        if (p.inject_stall && blockIdx.x == 0)  // test hook: a wait that runs out
+            ok = wait_warp(stall, 0, abort_flag, status, kGStStall, p.timeout_ns);
+        auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+            if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
+            else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
+        };
+        for (Walk w(unit); ok && w.next(p);) {
+            const int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM, n0 = (w.tile / p.mt) * p.cols;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
+                if (use > 0 && !(ok = wait_warp(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns))) break;
+                const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+                if (leader) {
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(kCtas * (p.a_bytes + p.b_bytes)));
                     if (MODE == kGFwd) {
                         load(sa, &tmA0, kb * kGKBlock, row0);
@@ -316,17 +350,21 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         for (int b = 0; b < p.b_bytes / 8192; ++b)
                             load(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, c0 + b * 64, f0);
                     }
-                    next();
+                }
+                __syncwarp();
+                if (++st == p.stages) {
+                    st = 0;
+                    ++use;
                 }
             }
-            if (PAIR) {  // landed below, once both producers have stopped
-                for (int s = 0; s < p.stages; ++s) s_fills[s] = use + (s < st ? 1 : 0);
-            } else {
-                // every copy this CTA issued lands before it leaves: the last fill of each stage
-                for (int s = 0; s < p.stages; ++s) {
-                    const uint32_t fills = use + (s < st ? 1 : 0);
-                    if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
-                }
+        }
+        if (PAIR) {  // landed below, once both producers have stopped
+            if (lane < p.stages) s_fills[lane] = use + (lane < st ? 1 : 0);
+        } else {
+            // every copy this CTA issued lands before it leaves: the last fill of each stage
+            for (int s = 0; s < p.stages; ++s) {
+                const uint32_t fills = use + (s < st ? 1 : 0);
+                if (fills) wait_warp(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
             }
         }
     } else if (warp == kGMma) {
@@ -354,9 +392,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         const uint64_t la0 = g_desc_k(lora_u);
         const uint64_t lb0 = MODE == kGFwd ? g_desc_mn(lora_bu, (uint32_t)(p.ups * 2048)) : g_desc_k64(lora_bu);
         const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4;
-        for (int t = rank == 0 ? tile0 : p.tiles; t < p.tiles && ok; t += tile_step, ++acc) {
-            const int m = t % p.mt, buf = acc & 1;
-            const int first = lora_first(p, t, tile0), spread = p.kb - first;
+        for (Walk w(unit); rank == 0 && ok && w.next(p); ++acc) {
+            const int m = w.tile % p.mt, buf = acc & 1;
+            const int first = w.lora_first(), spread = w.k1 - first;
             int blocks = LORA && waited ? p.list_len[m] : 0;
             if (acc >= 2 && !(ok = wait_warp(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
                                              p.timeout_ns)))
@@ -371,7 +409,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         const uint64_t da = da0 + (uint32_t)st * stage16, db = db0 + (uint32_t)st * stage16;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, (kb | ks) ? 1u : 0u);
+                            mma(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, kb > w.k0 || ks ? 1u : 0u);
                         commit(&empty[st]);
                     }
                     __syncwarp();
@@ -381,12 +419,12 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     }
                 }
             };
-            if (!LORA) {
-                main_stages(0, p.kb);
+            if (!LORA || w.k1 < p.kb) {  // a shared tile's last run has its LoRA steps
+                main_stages(w.k0, w.k1);
             } else {
                 // the tile's LoRA steps, evenly between the main stages from `first` on
                 int kb = first + 1, e = 0;
-                main_stages(0, kb);
+                main_stages(w.k0, kb);
                 if (ok && !waited) {
                     ptx::pdl_wait();
                     waited = true;
@@ -414,8 +452,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         }
                         __syncwarp();
                     }
-                    if (!ok || kb >= p.kb) break;
-                    const int n = ext ? min((spread - due + ext - 1) / ext, p.kb - kb) : p.kb - kb;
+                    if (!ok || kb >= w.k1) break;
+                    const int n = ext ? min((spread - due + ext - 1) / ext, w.k1 - kb) : w.k1 - kb;
                     main_stages(kb, kb + n);
                     kb += n;
                     due += n * ext;
@@ -451,29 +489,28 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                                                   : (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4)));
             uint8_t* bufs = ring + p.stages * p.stage_bytes;
 
-            // the walk over the steps: tile t, its step e of `ext`
-            int t = tile0, e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;
-            bool open = false;
+            // the walk over the steps: step e of `ext` of the tile
+            Walk w(unit);
+            int e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;
             int ids[kGMaxA];  // adapters of this builder's operand rows
             auto advance = [&]() -> bool {
-                for (;; t += tile_step, open = false) {
-                    if (t >= p.tiles) return false;
-                    if (!open) {
-                        m = t % p.mt;
-                        n0 = (t / p.mt) * p.cols + b_n0;
-                        row0 = m * kTokens + rank * kGTileM;
-                        blocks = p.list_len[m];
-                        ext = lora_steps(p, blocks);
-                        e = -1;
-                        open = true;
+                while (++e >= ext) {
+                    do
+                        if (!w.next(p)) return false;
+                    while (w.k1 < p.kb);
+                    m = w.tile % p.mt;
+                    n0 = (w.tile / p.mt) * p.cols + b_n0;
+                    row0 = m * kTokens + rank * kGTileM;
+                    blocks = p.list_len[m];
+                    ext = lora_steps(p, blocks);
+                    e = -1;
 #pragma unroll
-                        for (int i = 0; i < kGMaxA; ++i) {
-                            const int row = a_row + i * a_step, tok = row0 + row;
-                            ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
-                        }
+                    for (int i = 0; i < kGMaxA; ++i) {
+                        const int row = a_row + i * a_step, tok = row0 + row;
+                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
                     }
-                    if (++e < ext) return true;
                 }
+                return true;
             };
             // the blocks that the next step's pieces come from: one for the operand, one per pass of B
             int ua, ub[kGMaxB];
@@ -554,15 +591,72 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         // ================================================================ drain
         const int q = warp & 3, half = warp >> 2;
         int acc = 0;
-        for (int t = tile0; t < p.tiles; t += tile_step, ++acc) {
-            const int row0 = (t % p.mt) * kTokens + rank * kGTileM + q * 32, n0 = (t / p.mt) * p.cols, buf = acc & 1;
+        if (MODE == kGBwd && LORA && p.shared) ptx::pdl_wait();  // the counts were zeroed
+        for (Walk w(unit); w.next(p); ++acc) {
+            const int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM + q * 32, n0 = (w.tile / p.mt) * p.cols, buf = acc & 1;
             const int row = row0 + lane;
             if (!wait_role(3, kGDrainWarps * 32, threadIdx.x == 0, &tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status,
                            kGStDrain, p.timeout_ns))
                 break;
             ptx::tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGAccCols);
-            if (row0 < p.M) {  // the warp has live rows
+            bool mine = true;  // this CTA finishes the tile
+            if (MODE == kGBwd && w.piece >= 0) {
+                // a piece of a shared tile, to the workspace; the last one done takes the sum of all
+                // back into TMEM (sixteen loads in flight per thread) and finishes the tile
+                const int s = w.tile - p.whole;
+                const size_t piece4 = (size_t)kCtas * (p.bn / 4) * kGTileM;
+                float4* part = reinterpret_cast<float4*>(p.part) + (size_t)s * p.split * piece4 +
+                               (size_t)rank * (p.bn / 4) * kGTileM + q * 32 + lane;
+                if (row0 < p.M) {
+                    float4* dst = part + w.piece * piece4;
+                    for (int c = half * 32; c < p.bn; c += 64) {
+                        float v[32];
+                        ptx::tmem_ld32(ta + (uint32_t)c, v);
+                        if (row < p.M)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                __stcg(dst + (size_t)(c / 4 + i) * kGTileM, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                    }
+                }
+                __threadfence();
+                ptx::named_sync(4, kGDrainWarps * 32);
+                if (threadIdx.x == 0) s_last = atomicAdd(p.count + s * kCtas + rank, 1) == p.split - 1;
+                ptx::named_sync(4, kGDrainWarps * 32);
+                mine = s_last;
+                if (mine) {
+                    __threadfence();
+                    if (row0 < p.M)
+                        for (int c = half * 16; c < p.bn; c += 32) {
+                            float v[16] = {};
+                            for (int k0 = 0; k0 < p.split; k0 += 4) {
+                                float4 x[4][4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        x[k][i] = k0 + k < p.split
+                                                      ? __ldcg(part + (size_t)(k0 + k) * piece4 + (size_t)(c / 4 + i) * kGTileM)
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        v[4 * i] += x[k][i].x;
+                                        v[4 * i + 1] += x[k][i].y;
+                                        v[4 * i + 2] += x[k][i].z;
+                                        v[4 * i + 3] += x[k][i].w;
+                                    }
+                            }
+                            ptx::tmem_st16(ta + (uint32_t)c, v);
+                        }
+                    ptx::tc_fence_before();
+                    ptx::named_sync(4, kGDrainWarps * 32);  // the halves' columns of a row differ below
+                    ptx::tc_fence_after();
+                }
+            }
+            // the tile's outputs of this thread's row
+            if (mine && row0 < p.M) {  // the warp has live rows
                 if (MODE == kGFwd && p.g_codes) {
                     const int nb = (p.NC + act8::kBlock - 1) / act8::kBlock;
                     for (int c = half * 32; c < p.cols; c += 64) {
@@ -584,20 +678,24 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         }
                     }
                 } else {
-                    for (int c = half * 16; c < p.cols; c += 32) {
+                    constexpr int kN = MODE == kGFwd ? 16 : 32;
+                    for (int c = half * kN; c < p.cols; c += 2 * kN) {
                         const int col = n0 + c;
                         if (col >= p.NC) break;
-                        float g[16], u[16];
-                        ptx::tmem_ld16(ta + (uint32_t)c, g);
-                        if (MODE == kGFwd) {
+                        float g[kN], u[MODE == kGFwd ? kN : 1];
+                        if constexpr (MODE == kGFwd) {
+                            ptx::tmem_ld16(ta + (uint32_t)c, g);
                             ptx::tmem_ld16(ta + (uint32_t)(p.cols + c), u);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) g[i] = gate(p.act, g[i]) * u[i];
+                            for (int i = 0; i < kN; ++i) g[i] = gate(p.act, g[i]) * u[i];
+                        } else {
+                            ptx::tmem_ld32(ta + (uint32_t)c, g);
                         }
                         if (row < p.M) {
                             uint16_t* o = p.out + (size_t)row * p.NC + col;
-                            store_bf16x8(o, g);
-                            if (col + 8 < p.NC) store_bf16x8(o + 8, g + 8);
+#pragma unroll
+                            for (int i = 0; i < kN; i += 8)
+                                if (col + i < p.NC) store_bf16x8(o + i, g + i);
                         }
                     }
                 }
@@ -784,51 +882,69 @@ int pair_count()
 
 struct GatedPlan {
     bool pair;
-    int cols, mt, tiles, grid;
+    int cols, mt, tiles, units;
+    int split;  // pieces of the last round's tiles, 1: they stay whole
 };
 
-// The tiles of a call: the smallest of rounds x columns (rounds of the CTAs or pairs that run at
-// once) with a penalty on narrow tiles, whose stages carry fewer bytes per turn of the ring
-// and read their operands from shared memory more often per product; where one round holds all
-// tiles of a single token tile, narrower ones only bring in more SMs. (8192 x 28672, 16 tokens:
-// 112 columns in two rounds 6.1 TB/s of weights, 16 columns in thirteen 1.9 TB/s.) Single CTAs pay
-// an eighth for their shallower ring, so pairs take every call whose tiles fill them.
-GatedPlan gated_plan(bool bwd, int M, int NC, bool save)
+// A choice of tile: output columns, and the microseconds a CTA or pair takes per stage (64 of K)
+// with all of them at work, measured on 2048 tokens, 4096 x 11008. Pairs gain by their deeper ring;
+// narrow tiles read their operands from shared memory more often per product, and below 64
+// columns a stage takes the same time whatever its width.
+struct TileChoice {
+    bool pair;
+    int cols;
+    double us;
+};
+constexpr TileChoice kFwdTiles[] = {{true, 128, .373}, {true, 96, .309}, {true, 64, .267}, {false, 128, .411},
+                                    {false, 96, .329}, {false, 64, .292}, {false, 32, .30}, {false, 112, .364},
+                                    {false, 80, .304}, {false, 48, .30}, {false, 16, .30}};
+constexpr int kFwdSaveTiles = 7;  // with checkpoints: whole blocks of 32 columns
+constexpr TileChoice kBwdTiles[] = {{true, 256, .42}, {true, 128, .357}, {false, 256, .45}, {false, 128, .38}, {false, 64, .336}};
+constexpr double kShareUs = 40;  // what pieces have to gain: accumulators go out and in, the tail is longer
+constexpr int kMaxSplit = 16, kPieces = 3;  // pieces of a tile; of all tiles per unit, at most
+
+// The cheapest choice: rounds of the units over the tiles, whole or with the last one shared. A
+// single token tile is bound by the weights' stream instead: there time per stage goes by bytes
+// (8192 x 28672, 16 tokens: 112 columns in two rounds 6.4 TB/s, 16 columns in thirteen 2 TB/s).
+GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
 {
-    // output columns; forward with checkpoints: whole blocks of 32, and for pairs the adapters'
-    // MMA of half the columns wants 32 too
-    static const int fwd[] = {128, 96, 64, 32, 112, 80, 48, 16}, back[] = {256, 192, 128, 64};
-    static const double fwd_cost[] = {1, 1.04, 1.15, 1.8, 1.02, 1.08, 1.4, 3}, back_cost[] = {1, 1.04, 1.15, 1.8};
-    static const int fwd2[] = {128, 96, 64}, back2[] = {256, 128};
-    static const double fwd2_cost[] = {1, 1.04, 1.15}, back2_cost[] = {1, 1.15};
+    const int NC = bwd ? K : F, red = bwd ? 2 * ((F + 63) / 64) : (K + 63) / 64;
+    const TileChoice* tiles = bwd ? kBwdTiles : kFwdTiles;
+    const int n = bwd ? (int)(sizeof(kBwdTiles) / sizeof(TileChoice)) : (save ? kFwdSaveTiles : (int)(sizeof(kFwdTiles) / sizeof(TileChoice)));
+    const int pairs = M > kGTileM ? pair_count() : 0, sms = device_sm_count();
     GatedPlan best = {};
     double least = 0;
-    auto consider = [&](bool pair, const int* cols, const double* cost, int n, int units) {
-        const int mt = (M + (pair ? 255 : 127)) / (pair ? 256 : 128);
-        for (int i = 0; i < n; ++i) {
-            const long long tiles = (long long)mt * ((NC + cols[i] - 1) / cols[i]), rounds = (tiles + units - 1) / units;
-            const double v = (double)rounds * cols[i] * (rounds > 1 || mt > 1 || pair ? cost[i] : 1) * (pair ? 1 : 1.125);
-            if (best.cols && v >= least) continue;
-            least = v;
-            best.pair = pair;
-            best.cols = cols[i];
+    for (int i = 0; i < n; ++i) {
+        const TileChoice& c = tiles[i];
+        const int units = c.pair ? pairs : sms;
+        if (units < 1) continue;
+        const int mt = (M + (c.pair ? 255 : 127)) / (c.pair ? 256 : 128);
+        const long long all = (long long)mt * ((NC + c.cols - 1) / c.cols);
+        const double stream = (bwd ? .0028 : .0055) * c.cols, us = red * (mt == 1 && stream > c.us ? stream : c.us);
+        const long long rem = all % units;
+        for (int split = 1; split <= kMaxSplit; ++split) {
+            if (split > 1 && (!bwd || rem == 0 || rem * split > (long long)kPieces * units || red < 8 * split))
+                break;
+            const double last = (double)((rem * split + units - 1) / units) / split;
+            const double t = ((double)(all / units) + last) * us + (split > 1 ? kShareUs : 0);
+            if (best.cols && t >= least) continue;
+            least = t;
+            best.pair = c.pair;
+            best.split = split;
+            best.cols = c.cols;
             best.mt = mt;
-            best.tiles = (int)tiles;
-            best.grid = (int)(tiles < units ? tiles : units) * (pair ? 2 : 1);
+            best.tiles = (int)all;
+            best.units = (int)(split == 1 && all < units ? all : units);
         }
-    };
-    if (bwd) consider(false, back, back_cost, 4, device_sm_count());
-    else consider(false, fwd, fwd_cost, save ? 4 : 8, device_sm_count());
-    const int pairs = M > kGTileM ? pair_count() : 0;
-    if (pairs) {
-        if (bwd) consider(true, back2, back2_cost, 2, pairs);
-        else consider(true, fwd2, fwd2_cost, 3, pairs);
     }
     return best;
 }
 
 }  // namespace
 
+// Room for the pieces of the backward's shared tiles, and for their counts.
+size_t gated_part_bytes() { return (size_t)device_sm_count() * kPieces * kGTileM * kGAccCols * 4; }
+size_t gated_count_bytes() { return kGCounts * 4; }
 size_t gated_operand_bytes(int M, int r_max)
 {
     const size_t r16 = (size_t)(r_max + 15) / 16 * 16;
@@ -842,7 +958,7 @@ size_t gated_list_bytes(int M)
 cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
                                   bool backward, bool save, void* ops, void* lists, cudaStream_t stream)
 {
-    const GatedPlan plan = gated_plan(backward, M, backward ? pool.h_in : pool.h_out, save);
+    const GatedPlan plan = gated_plan(backward, M, pool.h_in, pool.h_out, save);
     OperandParams p = {};
     p.tile = plan.pair ? 2 * kGTileM : kGTileM;
     p.v = v;
@@ -877,11 +993,18 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     p.M = a.M;
     p.NC = bwd ? a.K : a.F;
     const bool save = a.g8 != nullptr;
-    const GatedPlan plan = gated_plan(bwd, a.M, p.NC, save);
+    const GatedPlan plan = gated_plan(bwd, a.M, a.K, a.F, save);
     p.mt = plan.mt;
     p.cols = plan.cols;
     p.bn = bwd ? p.cols : 2 * p.cols;
     p.tiles = plan.tiles;
+    p.units = plan.units;
+    p.split = plan.split;
+    p.rounds = plan.split > 1 ? plan.tiles / plan.units : (plan.tiles + plan.units - 1) / plan.units;
+    p.whole = plan.split > 1 ? p.rounds * plan.units : plan.tiles;
+    p.shared = plan.tiles - p.whole;
+    p.part = a.part;
+    p.count = a.count;
     const int red = bwd ? a.F : a.K;
     p.kb_half = (red + kGKBlock - 1) / kGKBlock;
     p.kb = bwd ? 2 * p.kb_half : p.kb_half;
@@ -940,12 +1063,13 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
                                   bwd ? kGKBlock : (uint32_t)p.cols, sw);
     }
     if (!ok) return cudaErrorInvalidValue;
+    const int grid = p.units * (plan.pair ? 2 : 1);
     if (plan.pair) {
-        if (bwd) return a.lora ? launch_mode<kGBwd, true, true>(tm, p, plan.grid, stream) : launch_mode<kGBwd, false, true>(tm, p, plan.grid, stream);
-        return a.lora ? launch_mode<kGFwd, true, true>(tm, p, plan.grid, stream) : launch_mode<kGFwd, false, true>(tm, p, plan.grid, stream);
+        if (bwd) return a.lora ? launch_mode<kGBwd, true, true>(tm, p, grid, stream) : launch_mode<kGBwd, false, true>(tm, p, grid, stream);
+        return a.lora ? launch_mode<kGFwd, true, true>(tm, p, grid, stream) : launch_mode<kGFwd, false, true>(tm, p, grid, stream);
     }
-    if (bwd) return a.lora ? launch_mode<kGBwd, true, false>(tm, p, plan.grid, stream) : launch_mode<kGBwd, false, false>(tm, p, plan.grid, stream);
-    return a.lora ? launch_mode<kGFwd, true, false>(tm, p, plan.grid, stream) : launch_mode<kGFwd, false, false>(tm, p, plan.grid, stream);
+    if (bwd) return a.lora ? launch_mode<kGBwd, true, false>(tm, p, grid, stream) : launch_mode<kGBwd, false, false>(tm, p, grid, stream);
+    return a.lora ? launch_mode<kGFwd, true, false>(tm, p, grid, stream) : launch_mode<kGFwd, false, false>(tm, p, grid, stream);
 }
 
 }  // namespace lora

@@ -32,7 +32,8 @@ struct PointParams {
     const uint16_t* dh;
     const uint8_t *g_codes, *g_scales, *u_codes, *u_scales;
     uint16_t *dg, *du, *h;
-    int F;
+    int* count;  // count_words words to zero
+    int count_words, F;
     uint32_t tasks, segs;
 };
 
@@ -57,6 +58,7 @@ gated_point_kernel(const PointParams p)
 {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
+    if (blockIdx.x == 0 && (int)threadIdx.x < p.count_words) p.count[threadIdx.x] = 0;
     const int lane = threadIdx.x & 31;
     const uint32_t stride = gridDim.x * kEWarps, nb = (uint32_t)((p.F + act8::kBlock - 1) / act8::kBlock);
     for (uint64_t t0 = blockIdx.x * kEWarps + (threadIdx.x >> 5); t0 < p.tasks; t0 += (uint64_t)stride * kEInFlight) {
@@ -468,9 +470,11 @@ cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
-                               void* dg, void* du, void* h, cudaStream_t stream)
+                               void* dg, void* du, void* h, int* count, cudaStream_t stream)
 {
     PointParams p = {};
+    p.count = count;
+    p.count_words = (int)(gated_count_bytes() / 4);  // at most a CTA's threads
     p.dh = static_cast<const uint16_t*>(dh);
     p.g_codes = g8.codes;
     p.g_scales = g8.scales;

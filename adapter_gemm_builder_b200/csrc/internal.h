@@ -84,6 +84,8 @@ cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, i
                                 const lora_segments_t& seg, float* v, int planes, cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
+size_t gated_part_bytes();
+size_t gated_count_bytes();
 cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
                                   bool backward, bool save, void* ops, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
@@ -95,6 +97,8 @@ struct GatedGemmArgs {
     const lora_act8_t* g8;  // forward: both or neither
     const lora_act8_t* u8;
     uint32_t* status;
+    float* part;            // backward: gated_part_bytes
+    int* count;             // backward: gated_count_bytes, zeroed by launch_gated_point
     bool lora;
     const void* ops;
     const void* lists;
@@ -105,8 +109,9 @@ struct GatedGemmArgs {
 // cudaErrorInvalidValue if an operand's tensor map is refused.
 cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream);
 // dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu).
+// Also zeroes `count` (gated_count_bytes).
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
-                               void* dg, void* du, void* h, cudaStream_t stream);
+                               void* dg, void* du, void* h, int* count, cudaStream_t stream);
 // Gradients of both slices: out[s][a][l][j] (long_rows) or [s][a][j][l] = the sum over the
 // adapter's tokens of lng[s][t][l] op[s][t][j], bf16; lng_slice 0: both slices read one lng.
 cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,

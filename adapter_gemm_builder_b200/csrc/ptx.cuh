@@ -506,6 +506,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v)
         v[i] = __uint_as_float(r[i]);
 }
 
+// The counterpart store: 16 consecutive columns of the thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v)
+{
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n"
+        "tcgen05.wait::st.sync.aligned;\n" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
 // The same for 32 consecutive columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v)
 {

@@ -29,7 +29,7 @@ def act64(kind, z):
     if kind == "silu":
         p = torch.sigmoid(z)
         return z * p, p * (1 + z * (1 - p))
-    P = torch.special.ndtr(z)
+    P = 0.5 * torch.erfc(-z * 0.5 ** 0.5)  # (special.ndtr loses its digits below -5: 6.1e-16 for 6.2e-16 at -8)
     return z * P, P + z * torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5
 
 
@@ -126,6 +126,8 @@ FORWARD = [
     # wide enough for pairs of CTAs: whole and ragged pairs, the odd CTA without tokens, many adapters
     (512, 128, 9600, 0, 8, "uniform"), (700, 136, 9496, 3, 16, "sorted_zipf"), (1100, 64, 5000, 300, 8, "uniform"),
     (2049, 72, 3000, 9, 64, "zipf"),
+    # tiles shared between CTAs: parts of a tile summed by whichever is done last
+    (300, 4096, 1000, 3, 16, "zipf"), (513, 2048, 5000, 2, 32, "sorted_zipf"), (130, 8192, 272, 40, 64, "uniform"),
 ]
 
 
@@ -138,7 +140,8 @@ def test_forward(M, K, F, n, r, ids, act):
 
 @pytest.mark.parametrize("M,K,F,n,r,ids", [(1, 64, 16, 0, 8, "uniform"), (5, 128, 48, 2, 8, "uniform"),
                                            (130, 256, 1040, 5, 16, "zipf"), (513, 200, 272, 3, 64, "sorted_zipf"),
-                                           (256, 64, 4112, 2, 32, "identical"), (600, 96, 9616, 4, 64, "sorted_zipf")])
+                                           (256, 64, 4112, 2, 32, "identical"), (600, 96, 9616, 4, 64, "sorted_zipf"),
+                                           (400, 4096, 1200, 3, 32, "zipf")])
 def test_forward_with_checkpoints(M, K, F, n, r, ids):
     """h as without them; a block's scale is the rule's for a largest element within the error of the
     sum, and an element is within half an E4M3 step (2^-4, or half the smallest step) of g or u."""
@@ -241,6 +244,9 @@ def check_backward(p, act, o):
     # pairs of CTAs
     (512, 9600, 80, 0, 8, "uniform", "silu", False, False), (900, 9576, 48, 5, 64, "sorted_zipf", "silu", False, True),
     (1281, 5008, 112, 200, 8, "uniform", "gelu", True, False),
+    # long sums: every tile shared, few tokens and many
+    (1, 128, 8192, 1, 16, "identical", "silu", False, False), (20, 1040, 4112, 7, 32, "uniform", "silu", True, True),
+    (300, 520, 6000, 0, 8, "uniform", "silu", False, False), (700, 1000, 3008, 6, 64, "zipf", "gelu", False, True),
 ])
 def test_backward(M, K, F, n, r, ids, act, x8, h):
     p = Problem(M, K, F, n, r, ids)
