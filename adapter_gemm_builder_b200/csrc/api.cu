@@ -133,9 +133,9 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
 }
 
 // Gated backward workspace: status | counts | parts of shared tiles | dg, du | with adapters:
-// x expanded | planes of u, then of v | operands of u, of v | rank blocks.
+// x expanded | planes of u, of v | operands of u, of v | rank blocks.
 struct GatedBwdWs {
-    size_t count, part, d, x, v, ops_u, ops_v, lists, size;
+    size_t count, part, d, x, u, v, ops_u, ops_v, lists, size;
 };
 GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 {
@@ -148,9 +148,10 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
     if (!pool) return w;
     w.x = w.size;
     w.size += align256((size_t)M * pool->h_in * 2);
+    w.u = w.size;
+    w.size += align256(apply_v_bytes(M, *pool, gated_shrink_planes(M, F, pool->n_adapters)));
     w.v = w.size;
-    const int a = gated_shrink_planes(M, F, pool->n_adapters), b = gated_shrink_planes(M, pool->h_in, pool->n_adapters);
-    w.size += align256(apply_v_bytes(M, *pool, a > b ? a : b));
+    w.size += align256(apply_v_bytes(M, *pool, gated_shrink_planes(M, pool->h_in, pool->n_adapters)));
     w.ops_u = w.size;
     w.size += align256(gated_operand_bytes(M, pool->r_max));
     w.ops_v = w.size;
@@ -160,15 +161,13 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
     return w;
 }
 
-// v = x.A (down) or d.B^T of both slices into planes at v, then its operands and the token tiles'
-// rank blocks.
-cudaError_t gated_operands(bool down, bool save, const void* lng, int64_t lng_slice, const lora_pool_t& pool,
-                           const lora_segments_t& seg, int M, float* v, void* ops, void* lists, cudaStream_t s)
+// v = x.A (down) or d.B^T of both slices of each side, then its operands and the token tiles' rank blocks.
+cudaError_t gated_operands(const GatedSide* sides, int n, bool backward, bool save, const lora_pool_t& pool,
+                           const lora_segments_t& seg, int M, void* lists, cudaStream_t s)
 {
-    const int L = down ? pool.h_in : pool.h_out, planes = gated_shrink_planes(M, L, pool.n_adapters);
-    const cudaError_t e = launch_gated_shrink(down, lng, lng_slice, L, M, pool, seg, v, planes, s);
+    const cudaError_t e = launch_gated_shrink(sides, n, M, pool, seg, s);
     if (e != cudaSuccess) return e;
-    return launch_gated_operands(v, planes, pool, seg, M, !down, save, ops, lists, s);
+    return launch_gated_operands(sides, n, M, pool, seg, backward, save, lists, s);
 }
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
@@ -659,9 +658,8 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
-        if (gated_operands(true, g8 != nullptr, x, 0, *pool, *seg, M, reinterpret_cast<float*>(w + l.v), w + l.ops, w + l.lists,
-                           s) != cudaSuccess)
-            return LORA_ERR_CUDA;
+        const GatedSide side = {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops};
+        if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
         a.lora = true;
         a.ops = w + l.ops;
         a.lists = w + l.lists;
@@ -712,10 +710,14 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.part = reinterpret_cast<float*>(w + l.part);
     a.count = count;
     if (!pool) return cuda_status(launch_gated_gemm(a, s));
-    // 2. u = d.B^T of both slices
-    float* v = reinterpret_cast<float*>(w + l.v);
-    if (gated_operands(false, false, dg, (int64_t)M * F, *pool, *seg, M, v, w + l.ops_u, w + l.lists, s) != cudaSuccess)
-        return LORA_ERR_CUDA;
+    // 2. u = d.B^T and v = x.A of both slices
+    if (x8) {
+        if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
+        x = w + l.x;
+    }
+    const GatedSide sides[2] = {{false, dg, (int64_t)M * F, reinterpret_cast<float*>(w + l.u), w + l.ops_u},
+                                {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops_v}};
+    if (gated_operands(sides, 2, true, false, *pool, *seg, M, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
     a.ops = w + l.ops_u;
@@ -725,16 +727,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.n_adapters = pool->n_adapters;
     a.r_max = pool->r_max;
     if (launch_gated_gemm(a, s) != cudaSuccess) return LORA_ERR_CUDA;
-    // 4. v = x.A, then the adapters' gradients
-    if (x8) {
-        if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
-        x = w + l.x;
-    }
-    if (gated_operands(true, false, x, 0, *pool, *seg, M, v, w + l.ops_v, w + l.lists, s) != cudaSuccess ||
-        launch_gated_outer(true, x, 0, K, w + l.ops_u, M, *pool, *seg, dA, s) != cudaSuccess ||
-        launch_gated_outer(false, dg, (int64_t)M * F, F, w + l.ops_v, M, *pool, *seg, dB, s) != cudaSuccess)
-        return LORA_ERR_CUDA;
-    return LORA_OK;
+    // 4. the adapters' gradients
+    return cuda_status(launch_gated_outer(x, w + l.ops_u, dA, dg, w + l.ops_v, dB, M, *pool, *seg, s));
 }
 
 int lora_switch_merge(const void* W, int N, int K, const lora_pool_t* pool, const int32_t* sel,

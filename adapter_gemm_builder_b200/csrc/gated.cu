@@ -18,7 +18,7 @@
 // B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is stored). v is split
 // into bf16 halves hi + lo that add up in the accumulator (16 bits of v). The steps have shared
 // memory of their own beside the ring and are spread between the main stages (in a CTA's first
-// tile over its second half, so that the shrink runs under the first half); the builders
+// tile from its second quarter on, so that the shrink runs under the first); the builders
 // have a step's data in registers before its buffer is free, and nothing that a load
 // depends on is fetched in the same step. (Steps in ring slots, loaded when the slot was free,
 // had cost the ring about 2 us each: 36 tokens of 32 adapters took 160 us, 37 us without them.)
@@ -227,8 +227,8 @@ struct Walk {
         return true;
     }
     // the stage after which the tile's LoRA steps begin to be spread: a unit's first piece leaves the
-    // shrink its first half
-    __device__ __forceinline__ int lora_first() const { return seen == 1 ? k0 + (k1 - k0) / 2 : k0; }
+    // shrink its first quarter
+    __device__ __forceinline__ int lora_first() const { return seen == 1 ? k0 + (k1 - k0) / 4 : k0; }
 };
 // A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has.
 __device__ __forceinline__ int block_code(int adapter, int block, int live) { return adapter << 8 | block << 6 | live; }
@@ -740,15 +740,17 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 // ------------------------------------------------------------------ LoRA operands
 
 struct OperandParams {
-    const float* v;  // `planes` planes of [2][M][r_max], summed in plane order
-    int planes;
+    struct {
+        const float* v;  // `planes` planes of [2][M][r_max], summed in plane order
+        int planes;
+        uint16_t* ops;
+    } side[2];           // blockIdx.y; the lists are made with the first
     long long plane;
     const int32_t* tok_adapter;
     const int32_t* ranks;
     const float* scales;
     int M, n_adapters, r_max, r16;
     int tile;  // tokens a list covers: 128 or 256
-    uint16_t* ops;
     int32_t* lists;
     int32_t* list_len;
 };
@@ -764,6 +766,7 @@ operand_kernel(const OperandParams p)
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto& d = p.side[blockIdx.y];
     const int chunks = p.r16 >> 3, items = 2 * kOpRows * chunks;
     for (int i = tid; i < items; i += kOpThreads) {
         const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
@@ -775,8 +778,8 @@ operand_kernel(const OperandParams p)
         const float scale = p.scales ? p.scales[a] : 1.f;
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (8 * c < r) {
-            const float* src = p.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
-            for (int k = 0; k < p.planes; ++k) {
+            const float* src = d.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
+            for (int k = 0; k < d.planes; ++k) {
                 const float4 x = *reinterpret_cast<const float4*>(src + k * p.plane);
                 const float4 y = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
                 f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
@@ -785,7 +788,7 @@ operand_kernel(const OperandParams p)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
-        uint4* o = reinterpret_cast<uint4*>(p.ops + ((size_t)s * p.M + row) * (2 * p.r16));
+        uint4* o = reinterpret_cast<uint4*>(d.ops + ((size_t)s * p.M + row) * (2 * p.r16));
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             uint32_t w[4];
@@ -799,7 +802,7 @@ operand_kernel(const OperandParams p)
         }
     }
     const int per = p.tile / kOpRows, m = (int)blockIdx.x / per;
-    if ((int)blockIdx.x % per) return;  // one CTA of the tile makes its list
+    if (blockIdx.y || (int)blockIdx.x % per) return;  // one CTA of the tile makes its list
     __shared__ int s_id[kOpThreads];
     __shared__ int s_cnt[kOpThreads / 32];
     const int row = m * p.tile + tid;
@@ -955,14 +958,17 @@ size_t gated_list_bytes(int M)
     return (size_t)(M + 2 * kGTileM - 1) / (2 * kGTileM) * 2 * (kListMax + 1) * 4;
 }
 
-cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
-                                  bool backward, bool save, void* ops, void* lists, cudaStream_t stream)
+cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
+                                  bool backward, bool save, void* lists, cudaStream_t stream)
 {
     const GatedPlan plan = gated_plan(backward, M, pool.h_in, pool.h_out, save);
     OperandParams p = {};
     p.tile = plan.pair ? 2 * kGTileM : kGTileM;
-    p.v = v;
-    p.planes = planes;
+    for (int i = 0; i < n; ++i) {
+        p.side[i].v = sides[i].v;
+        p.side[i].planes = gated_shrink_planes(M, sides[i].down ? pool.h_in : pool.h_out, pool.n_adapters);
+        p.side[i].ops = static_cast<uint16_t*>(sides[i].ops);
+    }
     p.plane = (long long)pool.n_slices * M * pool.r_max;
     p.tok_adapter = seg.tok_adapter;
     p.ranks = pool.ranks;
@@ -971,11 +977,10 @@ cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t&
     p.n_adapters = pool.n_adapters;
     p.r_max = pool.r_max;
     p.r16 = (pool.r_max + 15) / 16 * 16;
-    p.ops = static_cast<uint16_t*>(ops);
     p.lists = static_cast<int32_t*>(lists);
     p.list_len = p.lists + (size_t)plan.mt * kListMax * (p.tile / kGTileM);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(plan.mt * (p.tile / kOpRows)), 1, 1);
+    cfg.gridDim = dim3((unsigned)(plan.mt * (p.tile / kOpRows)), (unsigned)n, 1);
     cfg.blockDim = dim3(kOpThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -129,19 +129,24 @@ gated_point_kernel(const PointParams p)
 // tokens get zeros.
 
 constexpr int kOThreads = 128;
-constexpr int kOTok = 64;
+constexpr int kOTok = 64;    // tokens per step (shrink: of a CTA)
 constexpr int kOL = 64;
 constexpr int kOStages = 3;
 
-struct OuterParams {
+struct OuterSide {
     const uint16_t* lng;
     long long lng_slice;
     const uint16_t* ops;  // [2][M][hi r16 | lo r16]
     uint16_t* out;        // dA [2][n][L][r_max] or dB [2][n][r_max][L]
+    int L;
+};
+struct OuterParams {
+    OuterSide a, b;  // dA, dB
+    int a_blocks;    // CTAs of dA along the grid's x, then those of dB
     const int32_t* perm;
     const int32_t* indptr;
     const int32_t* ranks;
-    int M, L, n_adapters, r_max;
+    int M, n_adapters, r_max;
 };
 
 // Byte offset of 16-byte chunk c of row t, rows of CH chunks, laid out so that eight
@@ -154,38 +159,41 @@ __device__ __forceinline__ uint32_t o_chunk(int t, int c)
     return (uint32_t)(t * CH * 16 + ((c ^ (t & 7)) << 4));
 }
 
-template <bool LONG_ROWS, int R16>
+// T tokens per step.
+template <int R16, int T>
 __global__ void __launch_bounds__(kOThreads)
 gated_outer_kernel(const OuterParams p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kOpCh = R16 / 4;               // 16-byte chunks of an operand row (hi and lo)
-    constexpr int kLngBytes = kOTok * kOL * 2, kOpBytes = kOTok * kOpCh * 16, kStage = kLngBytes + kOpBytes;
+    constexpr int kLngBytes = T * kOL * 2, kOpBytes = T * kOpCh * 16, kStage = kLngBytes + kOpBytes;
     constexpr int NT = R16 / 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    const int l0 = (int)blockIdx.x * kOL, a = (int)blockIdx.y, s = (int)blockIdx.z;
+    const bool long_rows = (int)blockIdx.x < p.a_blocks;
+    const OuterSide& d = long_rows ? p.a : p.b;
+    const int l0 = ((int)blockIdx.x - (long_rows ? 0 : p.a_blocks)) * kOL, a = (int)blockIdx.y, s = (int)blockIdx.z;
     const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
     const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
-    const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
-    const uint16_t* ops = p.ops + (size_t)s * p.M * (2 * R16);
+    const uint16_t* lng = d.lng + (size_t)s * d.lng_slice;
+    const uint16_t* ops = d.ops + (size_t)s * p.M * (2 * R16);
     const uint32_t base = ptx::smem_u32(smem);
-    const int steps = (n_tok + kOTok - 1) / kOTok;
+    const int steps = (n_tok + T - 1) / T;
 
     auto fetch = [&](int step) {
         if (step < steps) {
             const uint32_t st = base + (uint32_t)((step % kOStages) * kStage);
 #pragma unroll
-            for (int i = 0; i < kOTok * (kOL / 8) / kOThreads; ++i) {
-                const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * kOTok + t;
-                const bool in = pos < n_tok && l0 + c * 8 < p.L;
-                const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * p.L + l0 + c * 8 : lng;
+            for (int i = 0; i < T * (kOL / 8) / kOThreads; ++i) {
+                const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * T + t;
+                const bool in = pos < n_tok && l0 + c * 8 < d.L;
+                const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * d.L + l0 + c * 8 : lng;
                 ptx::cp_async16(st + o_chunk<8>(t, c), src, in ? 16 : 0);
             }
 #pragma unroll
-            for (int i = 0; i < kOTok * kOpCh / kOThreads; ++i) {
-                const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * kOTok + t;
+            for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
+                const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * T + t;
                 const bool in = pos < n_tok;
                 const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
                 ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
@@ -207,7 +215,7 @@ gated_outer_kernel(const OuterParams p)
         const uint32_t st = base + (uint32_t)((step % kOStages) * kStage), so = st + kLngBytes;
         const int i = lane >> 3, rr = lane & 7;
 #pragma unroll
-        for (int ks = 0; ks < kOTok / 16; ++ks) {
+        for (int ks = 0; ks < T / 16; ++ks) {
             uint32_t A[4];
             ptx::ldsm_x4_t(st + o_chunk<8>(ks * 16 + (i >> 1) * 8 + rr, warp * 2 + (i & 1)), A[0], A[1], A[2], A[3]);
 #pragma unroll
@@ -225,7 +233,7 @@ gated_outer_kernel(const OuterParams p)
     ptx::cp_async_wait<0>();
     // one rounding to the adapters' type; columns past the rank are zero
     const int g = lane >> 2, q = lane & 3;
-    if (LONG_ROWS) {
+    if (long_rows) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int j = n * 8 + q * 2;
@@ -233,8 +241,8 @@ gated_outer_kernel(const OuterParams p)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int l = l0 + warp * 16 + g + h * 8;
-                if (l < p.L)
-                    *reinterpret_cast<uint32_t*>(p.out + (((size_t)s * p.n_adapters + a) * p.L + l) * p.r_max + j) =
+                if (l < d.L)
+                    *reinterpret_cast<uint32_t*>(d.out + (((size_t)s * p.n_adapters + a) * d.L + l) * p.r_max + j) =
                         pack_bf16x2(j < r ? acc[n][2 * h] : 0.f, j + 1 < r ? acc[n][2 * h + 1] : 0.f);
             }
         }
@@ -252,8 +260,8 @@ gated_outer_kernel(const OuterParams p)
         __syncthreads();
         for (int idx = tid; idx < p.r_max * (kOL / 8); idx += kOThreads) {
             const int j = idx >> 3, c = idx & 7, l = l0 + c * 8;
-            if (l < p.L)
-                *reinterpret_cast<uint4*>(p.out + (((size_t)s * p.n_adapters + a) * p.r_max + j) * p.L + l) =
+            if (l < d.L)
+                *reinterpret_cast<uint4*>(d.out + (((size_t)s * p.n_adapters + a) * p.r_max + j) * d.L + l) =
                     *reinterpret_cast<const uint4*>(o + j * kPitch + c * 8);
         }
     }
@@ -268,43 +276,46 @@ gated_outer_kernel(const OuterParams p)
 // m16n8k16: the products are 2 r16 per element of lng, few beside reading it, so HBM bounds it.
 // A warp owns 16 tokens; 64 values of l at a time come by cp.async into three stages.
 
-struct ShrinkParams {
+// One side of the sum: x against A (down) or d against B.
+struct ShrinkSide {
     const uint16_t* lng;
     long long lng_slice;
     const uint16_t* w;  // A [2][n][L][r_max] or B [2][n][r_max][L]
     float* v;           // [planes][2][M][r_max]
+    int L, planes, steps;  // steps of 64 per plane
+    bool down;
+};
+struct ShrinkParams {
+    ShrinkSide side[2];
     const int32_t* perm;
     const int4* tiles;
-    int M, L, n_adapters, r_max, planes, steps;  // steps of 64 per plane
+    int M, n_adapters, r_max;
 };
 
+// R16 ranks; DOWN: the rows of w are l.
 template <bool DOWN, int R16>
-__global__ void __launch_bounds__(kOThreads)
-gated_shrink_kernel(const ShrinkParams p)
+__device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const ShrinkSide& d, uint8_t* smem)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kLngBytes = kOTok * 128, kWBytes = R16 * 128, kStage = kLngBytes + kWBytes;
     constexpr int kWCh = DOWN ? R16 / 8 : 8;  // 16-byte pieces of a w row
     constexpr int kWRows = DOWN ? 64 : R16;
     constexpr int kWPer = kWRows * kWCh / kOThreads;  // pieces per thread
     constexpr int NT = R16 / 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
-    const int plane = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int plane = (int)blockIdx.y, s = (int)blockIdx.z & 1;
     const int4 tl = p.tiles[blockIdx.x];
     const int a = tl.x, n_tok = min(tl.z, kOTok);
     if (a < 0 || a >= p.n_adapters || n_tok <= 0) return;
-    const uint16_t* lng = p.lng + (size_t)s * p.lng_slice;
-    const uint16_t* w = p.w + ((size_t)s * p.n_adapters + a) * p.r_max * p.L;
+    const uint16_t* lng = d.lng + (size_t)s * d.lng_slice;
+    const uint16_t* w = d.w + ((size_t)s * p.n_adapters + a) * p.r_max * d.L;
     const uint32_t base = ptx::smem_u32(smem);
-    const int k0 = plane * p.steps, k1 = min(k0 + p.steps, (p.L + 63) / 64);
+    const int k0 = plane * d.steps, k1 = min(k0 + d.steps, (d.L + 63) / 64);
     // this thread's token rows
     const uint16_t* rows[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = (tid >> 3) + 16 * i;
-        rows[i] = t < n_tok ? lng + (size_t)p.perm[tl.y + t] * p.L : nullptr;
+        rows[i] = t < n_tok ? lng + (size_t)p.perm[tl.y + t] * d.L : nullptr;
     }
     auto fetch = [&](int k) {
         if (k < k1) {
@@ -313,14 +324,14 @@ gated_shrink_kernel(const ShrinkParams p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = (tid >> 3) + 16 * i, c = tid & 7;
-                const bool in = rows[i] && l0 + c * 8 < p.L;
+                const bool in = rows[i] && l0 + c * 8 < d.L;
                 ptx::cp_async16(st + o_chunk<8>(t, c), in ? rows[i] + l0 + c * 8 : lng, in ? 16 : 0);
             }
 #pragma unroll
             for (int i = 0; i < kWPer; ++i) {
                 const int idx = tid + i * kOThreads, t = idx / kWCh, c = idx % kWCh;
-                const bool in = DOWN ? l0 + t < p.L && c * 8 < p.r_max : t < p.r_max && l0 + c * 8 < p.L;
-                const uint16_t* src = DOWN ? w + (size_t)(l0 + t) * p.r_max + c * 8 : w + (size_t)t * p.L + l0 + c * 8;
+                const bool in = DOWN ? l0 + t < d.L && c * 8 < p.r_max : t < p.r_max && l0 + c * 8 < d.L;
+                const uint16_t* src = DOWN ? w + (size_t)(l0 + t) * p.r_max + c * 8 : w + (size_t)t * d.L + l0 + c * 8;
                 ptx::cp_async16(st + kLngBytes + o_chunk<kWCh>(t, c), in ? src : w, in ? 16 : 0);
             }
         }
@@ -361,12 +372,26 @@ gated_shrink_kernel(const ShrinkParams p)
     for (int h = 0; h < 2; ++h) {
         const int t = warp * 16 + g + h * 8;
         if (t >= n_tok) continue;
-        float* o = p.v + (((size_t)plane * 2 + s) * p.M + p.perm[tl.y + t]) * p.r_max;
+        float* o = d.v + (((size_t)plane * 2 + s) * p.M + p.perm[tl.y + t]) * p.r_max;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (n * 8 < p.r_max)
                 *reinterpret_cast<float2*>(o + n * 8 + q * 2) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
     }
+}
+
+// Grid: tile rows x planes x (side, slice).
+template <int R16>
+__global__ void __launch_bounds__(kOThreads)
+gated_shrink_kernel(const ShrinkParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const ShrinkSide& d = p.side[blockIdx.z >> 1];
+    if ((int)blockIdx.y >= d.planes) return;
+    if (d.down) shrink_tile<true, R16>(p, d, smem);
+    else shrink_tile<false, R16>(p, d, smem);
 }
 
 // The down shrink of a decode-like batch: a CTA takes a token, a slice and a plane's part of
@@ -381,15 +406,16 @@ gated_shrink_token_kernel(const ShrinkParams p, const int32_t* __restrict__ tok_
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int t = (int)blockIdx.x, plane = (int)blockIdx.y, s = (int)blockIdx.z;
+    const ShrinkSide& d = p.side[0];
     const int a = tok_adapter[t];
     if (a < 0 || a >= p.n_adapters) return;
-    const uint16_t* x = p.lng + (size_t)s * p.lng_slice + (size_t)t * p.L;
-    const uint16_t* w = p.w + ((size_t)s * p.n_adapters + a) * p.r_max * p.L;
+    const uint16_t* x = d.lng + (size_t)s * d.lng_slice + (size_t)t * d.L;
+    const uint16_t* w = d.w + ((size_t)s * p.n_adapters + a) * p.r_max * d.L;
     const int pieces = p.r_max >> 3, c = tid & (pieces - 1), step = kOThreads / pieces;
-    const int l1 = min((plane + 1) * p.steps * 64, p.L);
+    const int l1 = min((plane + 1) * d.steps * 64, d.L);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     constexpr int kAhead = 8;
-    for (int l = plane * p.steps * 64 + tid / pieces; l < l1; l += kAhead * step) {
+    for (int l = plane * d.steps * 64 + tid / pieces; l < l1; l += kAhead * step) {
         uint4 wv[kAhead];
         float xv[kAhead];
 #pragma unroll
@@ -423,19 +449,20 @@ gated_shrink_token_kernel(const ShrinkParams p, const int32_t* __restrict__ tok_
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < kOThreads / 32; ++i) v += s_sum[i][tid];
-        p.v[(((size_t)plane * 2 + s) * p.M + t) * p.r_max + tid] = v;
+        d.v[(((size_t)plane * 2 + s) * p.M + t) * p.r_max + tid] = v;
     }
 }
 
-template <bool DOWN, int R16>
-cudaError_t launch_shrink(const ShrinkParams& p, int rows, cudaStream_t stream)
+template <int R16>
+cudaError_t launch_shrink(const ShrinkParams& p, int sides, int rows, cudaStream_t stream)
 {
     const size_t smem = (size_t)kOStages * (kOTok * 128 + R16 * 128);
-    auto kern = gated_shrink_kernel<DOWN, R16>;
+    auto kern = gated_shrink_kernel<R16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    const int planes = sides == 2 && p.side[1].planes > p.side[0].planes ? p.side[1].planes : p.side[0].planes;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows, (unsigned)p.planes, 2);
+    cfg.gridDim = dim3((unsigned)rows, (unsigned)planes, (unsigned)(2 * sides));
     cfg.blockDim = dim3(kOThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -447,15 +474,17 @@ cudaError_t launch_shrink(const ShrinkParams& p, int rows, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool LONG_ROWS, int R16>
+template <int R16, int T>
 cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 {
-    const size_t smem = (size_t)kOStages * (kOTok * kOL * 2 + kOTok * R16 * 4);
-    auto kern = gated_outer_kernel<LONG_ROWS, R16>;
+    size_t smem = (size_t)kOStages * (T * kOL * 2 + T * R16 * 4);
+    const size_t out = (size_t)R16 * (kOL + 8) * 2;  // dB's tile on its way out
+    if (smem < out) smem = out;
+    auto kern = gated_outer_kernel<R16, T>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.L + kOL - 1) / kOL), (unsigned)p.n_adapters, 2);
+    cfg.gridDim = dim3((unsigned)(p.a_blocks + (p.b.L + kOL - 1) / kOL), (unsigned)p.n_adapters, 2);
     cfg.blockDim = dim3(kOThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -465,6 +494,13 @@ cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Few tokens per adapter: short steps, whose buffers let more CTAs run on an SM.
+template <int R16>
+cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
+{
+    return p.M <= 32LL * p.n_adapters ? launch_outer<R16, 32>(p, stream) : launch_outer<R16, 64>(p, stream);
 }
 
 }  // namespace
@@ -512,25 +548,29 @@ int gated_shrink_planes(int M, int L, int n_adapters)
     return (int)(planes < 1 ? 1 : (planes > 8 ? 8 : planes));
 }
 
-cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, int L, int M, const lora_pool_t& pool,
-                                const lora_segments_t& seg, float* v, int planes, cudaStream_t stream)
+cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
+                                cudaStream_t stream)
 {
     ShrinkParams p = {};
-    p.lng = static_cast<const uint16_t*>(lng);
-    p.lng_slice = lng_slice;
-    p.w = static_cast<const uint16_t*>(down ? pool.A : pool.B);
-    p.v = v;
+    for (int i = 0; i < n; ++i) {
+        ShrinkSide& d = p.side[i];
+        d.down = sides[i].down;
+        d.lng = static_cast<const uint16_t*>(sides[i].lng);
+        d.lng_slice = sides[i].lng_slice;
+        d.w = static_cast<const uint16_t*>(d.down ? pool.A : pool.B);
+        d.v = sides[i].v;
+        d.L = d.down ? pool.h_in : pool.h_out;
+        d.planes = gated_shrink_planes(M, d.L, pool.n_adapters);
+        d.steps = ((d.L + 63) / 64 + d.planes - 1) / d.planes;
+    }
     p.perm = seg.perm;
     p.tiles = reinterpret_cast<const int4*>(seg.tiles);
     p.M = M;
-    p.L = L;
     p.n_adapters = pool.n_adapters;
     p.r_max = pool.r_max;
-    p.planes = planes;
-    p.steps = ((L + 63) / 64 + planes - 1) / planes;
-    if (down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
+    if (n == 1 && sides[0].down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)M, (unsigned)planes, 2);
+        cfg.gridDim = dim3((unsigned)M, (unsigned)p.side[0].planes, 2);
         cfg.blockDim = dim3(kOThreads, 1, 1);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
@@ -541,29 +581,34 @@ cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, i
         return cudaLaunchKernelEx(&cfg, gated_shrink_token_kernel, p, (const int32_t*)seg.tok_adapter);
     }
     const int rows = max_tiles_for(M, pool.n_adapters);
-    if (pool.r_max <= 16) return down ? launch_shrink<true, 16>(p, rows, stream) : launch_shrink<false, 16>(p, rows, stream);
-    if (pool.r_max == 32) return down ? launch_shrink<true, 32>(p, rows, stream) : launch_shrink<false, 32>(p, rows, stream);
-    return down ? launch_shrink<true, 64>(p, rows, stream) : launch_shrink<false, 64>(p, rows, stream);
+    if (pool.r_max <= 16) return launch_shrink<16>(p, n, rows, stream);
+    if (pool.r_max == 32) return launch_shrink<32>(p, n, rows, stream);
+    return launch_shrink<64>(p, n, rows, stream);
 }
 
-cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,
-                               const lora_pool_t& pool, const lora_segments_t& seg, void* out, cudaStream_t stream)
+cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
+                               const lora_pool_t& pool, const lora_segments_t& seg, cudaStream_t stream)
 {
     OuterParams p = {};
-    p.lng = static_cast<const uint16_t*>(lng);
-    p.lng_slice = lng_slice;
-    p.ops = static_cast<const uint16_t*>(ops);
-    p.out = static_cast<uint16_t*>(out);
+    p.a.lng = static_cast<const uint16_t*>(x);
+    p.a.ops = static_cast<const uint16_t*>(ops_u);
+    p.a.out = static_cast<uint16_t*>(dA);
+    p.a.L = pool.h_in;
+    p.b.lng = static_cast<const uint16_t*>(d);
+    p.b.lng_slice = (long long)M * pool.h_out;
+    p.b.ops = static_cast<const uint16_t*>(ops_v);
+    p.b.out = static_cast<uint16_t*>(dB);
+    p.b.L = pool.h_out;
+    p.a_blocks = (p.a.L + kOL - 1) / kOL;
     p.perm = seg.perm;
     p.indptr = seg.indptr;
     p.ranks = pool.ranks;
     p.M = M;
-    p.L = L;
     p.n_adapters = pool.n_adapters;
     p.r_max = pool.r_max;
-    if (pool.r_max <= 16) return long_rows ? launch_outer<true, 16>(p, stream) : launch_outer<false, 16>(p, stream);
-    if (pool.r_max == 32) return long_rows ? launch_outer<true, 32>(p, stream) : launch_outer<false, 32>(p, stream);
-    return long_rows ? launch_outer<true, 64>(p, stream) : launch_outer<false, 64>(p, stream);
+    if (pool.r_max <= 16) return launch_outer<16>(p, stream);
+    if (pool.r_max == 32) return launch_outer<32>(p, stream);
+    return launch_outer<64>(p, stream);
 }
 
 }  // namespace lora

@@ -70,24 +70,31 @@ cudaError_t launch_mxfp4_quantize(const void* W, int N, int K, uint8_t* Wp, uint
 cudaError_t launch_act8_compress(const void* x, int M, int N, const lora_act8_t& out, cudaStream_t stream);
 cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cudaStream_t stream);
 
-// The gated feed-forward block. launch_gated_operands turns `planes` planes of v
-// [2][M][r_max] into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
+// The gated feed-forward block. launch_gated_operands turns the planes of v
+// [2][M][r_max] of each side into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
 // lists the rank blocks of each token tile of the GEMM that follows (backward or not, saving
 // checkpoints or not; gated_list_bytes). With adapters the launches
 // right before launch_gated_gemm are a shrink that waits for its predecessors before it lets
 // its dependents start, then launch_gated_operands (gated.cu says why).
-// launch_gated_shrink: `planes` (gated_shrink_planes) planes of v[s][t][j] = sum_l lng[s][t][l] w,
-// w = pool.A[s][a][l][j] (down: x.A) or pool.B[s][a][j][l] (else: d.B^T), lng_slice 0: both
-// slices read one lng (gated_grad.cu).
+// launch_gated_shrink, for each of n sides: gated_shrink_planes planes of v[s][t][j] = sum_l
+// lng[s][t][l] w, w = pool.A[s][a][l][j] (down: x.A) or pool.B[s][a][j][l] (else: d.B^T), lng_slice
+// 0: both slices read one lng (gated_grad.cu).
+struct GatedSide {
+    bool down;
+    const void* lng;
+    int64_t lng_slice;
+    float* v;
+    void* ops;  // where launch_gated_operands puts the side's operands
+};
 int gated_shrink_planes(int M, int L, int n_adapters);
-cudaError_t launch_gated_shrink(bool down, const void* lng, int64_t lng_slice, int L, int M, const lora_pool_t& pool,
-                                const lora_segments_t& seg, float* v, int planes, cudaStream_t stream);
+cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
+                                cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
 size_t gated_part_bytes();
 size_t gated_count_bytes();
-cudaError_t launch_gated_operands(const float* v, int planes, const lora_pool_t& pool, const lora_segments_t& seg, int M,
-                                  bool backward, bool save, void* ops, void* lists, cudaStream_t stream);
+cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
+                                  bool backward, bool save, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
     bool backward;
     int M, K, F, act;
@@ -112,10 +119,10 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream);
 // Also zeroes `count` (gated_count_bytes).
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
                                void* dg, void* du, void* h, int* count, cudaStream_t stream);
-// Gradients of both slices: out[s][a][l][j] (long_rows) or [s][a][j][l] = the sum over the
-// adapter's tokens of lng[s][t][l] op[s][t][j], bf16; lng_slice 0: both slices read one lng.
-cudaError_t launch_gated_outer(bool long_rows, const void* lng, int64_t lng_slice, int L, const void* ops, int M,
-                               const lora_pool_t& pool, const lora_segments_t& seg, void* out, cudaStream_t stream);
+// Gradients of both slices, bf16: dA[s][a][k][j] = sum_t x[t][k] op_u[s][t][j] and dB[s][a][j][f] =
+// sum_t op_v[s][t][j] d[s][t][f] over the adapter's tokens.
+cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
+                               const lora_pool_t& pool, const lora_segments_t& seg, cudaStream_t stream);
 
 struct Fp8GemmArgs {
     int M, N, K;

@@ -356,10 +356,12 @@ def _need(ok: bool, what: str):
         raise LoraError(LORA_ERR_INVALID_ARG, what)
 
 
-def _rows(t, shape, what: str, device=None):
-    """A contiguous bf16 tensor of this shape on one CUDA device, as the library reads it."""
-    _need(t.is_cuda and t.dtype is torch.bfloat16 and tuple(t.shape) == tuple(shape) and t.is_contiguous()
-          and (device is None or t.device == device), f"{what}: contiguous bf16 {tuple(shape)} on one GPU")
+def _rows(t, shape, what: str, device=None) -> int:
+    """The address of a contiguous bf16 tensor of this shape on one CUDA device, as the library reads it."""
+    if not (t.is_cuda and t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous()
+            and (device is None or t.device == device)):
+        _need(False, f"{what}: contiguous bf16 {tuple(shape)} on one GPU")
+    return t.data_ptr()
 
 
 class Act8:
@@ -380,47 +382,57 @@ class Act8:
     def _hold(self, codes, scales):
         M, N = codes.shape
         _need(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
-              and scales.is_contiguous() and tuple(scales.shape) == (M, (N + 31) // 32)
+              and scales.is_contiguous() and scales.shape == (M, (N + 31) // 32)
               and codes.device == scales.device, "checkpoint: contiguous uint8 codes [M, N], scales [M, ceil(N / 32)]")
         self.codes, self.scales = codes, scales
+        self.shape = codes.shape
         self.c = lora_act8_t(codes.data_ptr(), scales.data_ptr())
-
-    @property
-    def shape(self): return self.codes.shape
+        self._ref = ctypes.byref(self.c)
 
 
 def _act8(a: "Act8 | None", shape, what: str, device=None):
     """Its C struct, or NULL."""
     if a is None:
         return None
-    _need(a.codes.is_cuda and tuple(a.shape) == tuple(shape) and (device is None or a.codes.device == device),
-          f"{what}: a checkpoint of {tuple(shape)} on one GPU")
-    return ctypes.byref(a.c)
+    if not (a.codes.is_cuda and a.shape == shape and (device is None or a.codes.device == device)):
+        _need(False, f"{what}: a checkpoint of {tuple(shape)} on one GPU")
+    return a._ref
 
 
-def _on(device, stream):
-    """The device made current for a launch, and the stream (the device's current one by default)."""
-    return torch.cuda.device(device), _stream(torch.cuda.current_stream(device) if stream is None else stream)
+def _call(device, stream, name: str, *args):
+    """One library call with `device` current, on the stream (the device's current one by default)."""
+    f = getattr(_lib or load(), name)
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, s)
+    if status != LORA_OK:
+        _check(status)
 
 
 def act8_compress_rows(x: torch.Tensor, out: Act8, stream=None) -> None:
     """out = the 8-bit checkpoint of x (bf16 [M, N], N % 16 == 0)."""
     M, N = x.shape
-    _rows(x, (M, N), "x")
-    c = _act8(out, (M, N), "out", x.device)
-    guard, s = _on(x.device, stream)
-    with guard:
-        _check(load().act8_compress_rows(_ptr(x), M, N, c, s))
+    px = _rows(x, (M, N), "x")
+    _call(x.device, stream, "act8_compress_rows", px, M, N, _act8(out, (M, N), "out", x.device))
 
 
 def act8_expand_rows(a: Act8, x: torch.Tensor, stream=None) -> None:
     """x = the bf16 values that the checkpoint stands for."""
     M, N = a.shape
-    _rows(x, (M, N), "x")
-    c = _act8(a, (M, N), "a", x.device)
-    guard, s = _on(x.device, stream)
-    with guard:
-        _check(load().act8_expand_rows(c, M, N, _ptr(x), s))
+    px = _rows(x, (M, N), "x")
+    _call(x.device, stream, "act8_expand_rows", _act8(a, (M, N), "a", x.device), M, N, px)
+
+
+def _pool_on(pool: Pool | None, seg: Segments | None, device):
+    """C structs of the adapters and the batch's segments, or NULLs."""
+    if pool is None:
+        return None, None
+    _need(seg is not None and pool.A.device == device and seg.perm.device == device,
+          "pool, seg: on the other tensors' GPU")
+    return ctypes.byref(pool.c), ctypes.byref(seg.c)
 
 
 def bf16_gated_gemm_lora_epilogue(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, pool: Pool | None,
@@ -431,16 +443,14 @@ def bf16_gated_gemm_lora_epilogue(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.T
     M, K = x.shape
     F = Wg.shape[0]
     dev = x.device
-    _rows(x, (M, K), "x")
-    _rows(Wg, (F, K), "Wg", dev)
-    _rows(Wu, (F, K), "Wu", dev)
-    _rows(h, (M, F), "h", dev)
+    px = _rows(x, (M, K), "x")
+    pg, pu = _rows(Wg, (F, K), "Wg", dev), _rows(Wu, (F, K), "Wu", dev)
+    ph = _rows(h, (M, F), "h", dev)
+    _need(ws.device == dev, "ws: on the other tensors' GPU")
+    pool_c, seg_c = _pool_on(pool, seg, dev)
     g8, u8 = (None, None) if save is None else (_act8(save[0], (M, F), "save[0]", dev), _act8(save[1], (M, F), "save[1]", dev))
-    guard, s = _on(dev, stream)
-    with guard:
-        _check(load().bf16_gated_gemm_lora_epilogue(
-            _ptr(x), M, K, F, _ptr(Wg), _ptr(Wu), act, ctypes.byref(pool.c) if pool else None,
-            ctypes.byref(seg.c) if seg else None, _ptr(h), g8, u8, _ptr(ws), ws.numel(), s))
+    _call(dev, stream, "bf16_gated_gemm_lora_epilogue", px, M, K, F, pg, pu, act, pool_c, seg_c, ph, g8, u8,
+          ws.data_ptr(), ws.numel())
 
 
 def bf16_gated_lora_backward(dh: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, pool: Pool | None,
@@ -453,27 +463,24 @@ def bf16_gated_lora_backward(dh: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tenso
     M, F = dh.shape
     K = Wg.shape[1]
     dev = dh.device
-    _rows(dh, (M, F), "dh")
-    _rows(Wg, (F, K), "Wg", dev)
-    _rows(Wu, (F, K), "Wu", dev)
-    _rows(dX, (M, K), "dX", dev)
-    if h is not None:
-        _rows(h, (M, F), "h", dev)
+    pd = _rows(dh, (M, F), "dh")
+    pg, pu = _rows(Wg, (F, K), "Wg", dev), _rows(Wu, (F, K), "Wu", dev)
+    pX = _rows(dX, (M, K), "dX", dev)
+    ph = None if h is None else _rows(h, (M, F), "h", dev)
     _need(g8 is not None and u8 is not None, "g8, u8: checkpoints of g and u")
-    x8 = x if isinstance(x, Act8) else None
+    _need(ws.device == dev, "ws: on the other tensors' GPU")
+    pool_c, seg_c = _pool_on(pool, seg, dev)
+    px = x8 = pA = pB = None
     if pool is not None:
         n, r = pool.c.n_adapters, pool.c.r_max
         _need(x is not None and dA is not None and dB is not None, "x, dA and dB: required with a pool")
-        _rows(dA, (2, n, K, r), "dA", dev)
-        _rows(dB, (2, n, r, F), "dB", dev)
-        if x8 is None:
-            _rows(x, (M, K), "x", dev)
-    guard, s = _on(dev, stream)
-    with guard:
-        _check(load().bf16_gated_lora_backward(
-            None if x8 is not None else _ptr(x), _act8(x8, (M, K), "x", dev), _ptr(dh), M, K, F, _ptr(Wg), _ptr(Wu), act,
-            ctypes.byref(pool.c) if pool else None, ctypes.byref(seg.c) if seg else None, _act8(g8, (M, F), "g8", dev),
-            _act8(u8, (M, F), "u8", dev), _ptr(h), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), s))
+        pA, pB = _rows(dA, (2, n, K, r), "dA", dev), _rows(dB, (2, n, r, F), "dB", dev)
+        if isinstance(x, Act8):
+            x8 = _act8(x, (M, K), "x", dev)
+        else:
+            px = _rows(x, (M, K), "x", dev)
+    _call(dev, stream, "bf16_gated_lora_backward", px, x8, pd, M, K, F, pg, pu, act, pool_c, seg_c,
+          _act8(g8, (M, F), "g8", dev), _act8(u8, (M, F), "u8", dev), ph, pX, pA, pB, ws.data_ptr(), ws.numel())
 
 
 def lora_switch_merge(W: torch.Tensor, pool: Pool, sel: torch.Tensor, gates: torch.Tensor,
