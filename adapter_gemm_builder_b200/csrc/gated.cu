@@ -18,9 +18,8 @@
 // B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is stored). v is split
 // into bf16 halves hi + lo that add up in the accumulator (16 bits of v). The steps have shared
 // memory of their own beside the ring and are spread between the main stages (in a CTA's first
-// tile from its second quarter on, so that the shrink runs under the first); the builders
-// have a step's data in registers before its buffer is free, and nothing that a load
-// depends on is fetched in the same step. (Steps in ring slots, loaded when the slot was free,
+// tile from its second quarter on, so that the shrink runs under the first); the builders copy
+// with cp.async, one step ahead of the one that they hand over where two buffers fit. (Steps in ring slots, loaded when the slot was free,
 // had cost the ring about 2 us each: 36 tokens of 32 adapters took 160 us, 37 us without them.)
 // Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
 // are sorted by adapter has few adapters per tile.
@@ -70,8 +69,9 @@ constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 12;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
 constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
-constexpr int kGSmemShort = 192 * 1024;       // the same with fewer than 128 tokens
+constexpr int kGSmemShort = 208 * 1024;       // the same with fewer than 128 tokens
 constexpr int kGBarBytes = 512;
+constexpr int kGMaxLora = 2;                  // LoRA step buffers
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
 constexpr int kGCounts = 256;                 // counts of shared tiles (fewer than units, two CTAs each)
 constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);  // rank blocks of 128 tokens
@@ -236,8 +236,11 @@ __device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
 __device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
 __device__ __forceinline__ int block_live(int u) { return u & 63; }
 constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
-// LoRA steps of a token tile with this many rank blocks, both slices.
+// LoRA steps of a token tile with this many rank blocks, both slices; a piece of a shared tile has
+// its share of them.
 __device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
+__device__ __forceinline__ int steps_begin(const GatedParams& p, int steps, int piece) { return piece < 0 ? 0 : steps * piece / p.split; }
+__device__ __forceinline__ int steps_end(const GatedParams& p, int steps, int piece) { return piece < 0 ? steps : steps * (piece + 1) / p.split; }
 // Where a step's B part begins: behind the operand's tiles of 64 columns (four groups of 16:
 // ups of hi, ups of lo).
 __host__ __device__ __forceinline__ uint32_t lora_b_offset(const GatedParams& p) { return (uint32_t)(p.ups / 2 * p.a_bytes); }
@@ -264,12 +267,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t raw_u = ptx::smem_u32(smem_raw);
     const uint32_t base_u = (raw_u + 1023u) & ~1023u;
-    uint8_t* ring = smem_raw + (base_u - raw_u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + p.smem - kGBarBytes);
     uint64_t* empty = full + kGMaxStages;
-    uint64_t* lfull = empty + kGMaxStages;  // [2] LoRA step buffers
-    uint64_t* lempty = lfull + 2;           // [2]
-    uint64_t* tfull = lempty + 2;
+    uint64_t* lfull = empty + kGMaxStages;  // LoRA step buffers
+    uint64_t* lempty = lfull + kGMaxLora;
+    uint64_t* tfull = lempty + kGMaxLora;
     uint64_t* tempty = tfull + 2;
     uint64_t* mdone = tempty + 2;
     uint64_t* stall = mdone + 1;  // test hook: never completed
@@ -282,9 +284,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kGMaxLora; ++b) {
             ptx::mbar_init(&lfull[b], kCtas);
             ptx::mbar_init(&lempty[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], kCtas * kGDrainWarps);
         }
@@ -374,7 +378,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         // longer than their 512 cycles of products: 2048 x 8192 x 11008 with adapters 645 us.)
         const bool leader = ptx::elect_one();
         int st = 0, acc = 0;
-        uint32_t use = 0, step = 0;  // turns of the ring; LoRA steps so far
+        uint32_t use = 0, lb = 0, turn = 0;  // turns of the ring; buffer of the next LoRA step, its turns
         bool ok = true, waited = false;
         const uint32_t id_main = g_idesc(kTokens, p.bn, MODE == kGBwd), id_lora = g_idesc(kTokens, p.cols, MODE == kGFwd);
         auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
@@ -419,11 +423,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     }
                 }
             };
-            if (!LORA || w.k1 < p.kb) {  // a shared tile's last run has its LoRA steps
+            if (!LORA) {
                 main_stages(w.k0, w.k1);
             } else {
                 // the tile's LoRA steps, evenly between the main stages from `first` on
-                int kb = first + 1, e = 0;
+                int kb = first + 1;
                 main_stages(w.k0, kb);
                 if (ok && !waited) {
                     ptx::pdl_wait();
@@ -431,11 +435,11 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     blocks = p.list_len[m];
                 }
                 blocks = __shfl_sync(0xffffffffu, blocks, 0);  // uniform, and so the walk
-                const int ext = lora_steps(p, blocks);
-                int due = ext;
+                const int all = lora_steps(p, blocks);
+                int e = steps_begin(p, all, w.piece), due = steps_end(p, all, w.piece) - e;
+                const int ext = due;
                 while (ok) {
-                    for (; due >= spread; due -= spread, ++e, ++step) {
-                        const uint32_t lb = p.lbufs == 2 ? step & 1 : 0, turn = p.lbufs == 2 ? step >> 1 : step;
+                    for (; due >= spread; due -= spread, ++e) {
                         if (!(ok = wait_warp(&lfull[lb], turn & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
                         ptx::tc_fence_after();
                         if (leader) {
@@ -451,6 +455,10 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             commit(&lempty[lb]);
                         }
                         __syncwarp();
+                        if (++lb == (uint32_t)p.lbufs) {
+                            lb = 0;
+                            ++turn;
+                        }
                     }
                     if (!ok || kb >= w.k1) break;
                     const int n = ext ? min((spread - due + ext - 1) / ext, w.k1 - kb) : w.k1 - kb;
@@ -487,23 +495,20 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             const uint32_t b_off =
                 lora_b_offset(p) + (MODE == kGFwd ? (uint32_t)((b_c >> 3) * (p.ups * 2048) + b_row * 128 + (((b_c & 7) ^ (b_row & 7)) << 4))
                                                   : (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4)));
-            uint8_t* bufs = ring + p.stages * p.stage_bytes;
-
             // the walk over the steps: step e of `ext` of the tile
             Walk w(unit);
-            int e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;
+            int e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;  // the tile's next step, where they end
             int ids[kGMaxA];  // adapters of this builder's operand rows
             auto advance = [&]() -> bool {
                 while (++e >= ext) {
-                    do
-                        if (!w.next(p)) return false;
-                    while (w.k1 < p.kb);
+                    if (!w.next(p)) return false;
                     m = w.tile % p.mt;
                     n0 = (w.tile / p.mt) * p.cols + b_n0;
                     row0 = m * kTokens + rank * kGTileM;
                     blocks = p.list_len[m];
-                    ext = lora_steps(p, blocks);
-                    e = -1;
+                    const int all = lora_steps(p, blocks);
+                    ext = steps_end(p, all, w.piece);
+                    e = steps_begin(p, all, w.piece) - 1;
 #pragma unroll
                     for (int i = 0; i < kGMaxA; ++i) {
                         const int row = a_row + i * a_step, tok = row0 + row;
@@ -525,67 +530,69 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     ub[i] = (MODE == kGFwd || i == 0) && kk < p.ups && kb < blocks ? list[kb] : kNoBlock;
                 }
             };
-            uint4 ra[kGMaxA], rb[kGMaxB];
-            auto load = [&]() {  // the step's pieces into registers; zero where nothing belongs
+            auto copy = [&](uint32_t buf) {  // the step's pieces into its buffer; zero where nothing belongs
                 const int s = e & 1;
                 const uint16_t* src = p.ops + (size_t)s * p.M * (2 * p.r16) + a_half * p.r16 + block_rank0(ua) + (a_k & 1) * 8;
 #pragma unroll
                 for (int i = 0; i < kGMaxA; ++i) {
-                    ra[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ids[i] == block_adapter(ua))
-                        ra[i] = *reinterpret_cast<const uint4*>(src + (size_t)(row0 + a_row + i * a_step) * (2 * p.r16));
+                    const bool in = ids[i] == block_adapter(ua);
+                    if (a_row + i * a_step < a_rows)
+                        ptx::cp_async16(buf + a_off + (uint32_t)(i * a_step * 128),
+                                        in ? src + (size_t)(row0 + a_row + i * a_step) * (2 * p.r16) : p.ops, in ? 16 : 0);
                 }
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i) {
                     const int row = b_row + i * b_step, u = MODE == kGFwd ? ub[i] : ub[0];
-                    rb[i] = make_uint4(0u, 0u, 0u, 0u);
-                    const size_t pool = ((size_t)s * p.n_adapters + block_adapter(u)) * p.r_max * p.NC;
+                    if (row >= b_rows) continue;
+                    const uint16_t* pool = p.B + ((size_t)s * p.n_adapters + block_adapter(u)) * p.r_max * p.NC;
                     if (MODE == kGFwd) {  // a row of B_a, eight columns
                         const int j = row & 15;
-                        if (row < b_rows && j < block_live(u) && n0 + b_c * 8 < p.NC)
-                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(block_rank0(u) + j) * p.NC + n0 + b_c * 8);
-                    } else {  // a row of A_a, eight ranks
-                        const int j = (b_c & 1) * 8;
-                        if (row < b_rows && j < block_live(u) && n0 + row < p.NC)
-                            rb[i] = *reinterpret_cast<const uint4*>(p.B + pool + (size_t)(n0 + row) * p.r_max + block_rank0(u) + j);
+                        const bool in = j < block_live(u) && n0 + b_c * 8 < p.NC;
+                        ptx::cp_async16(buf + b_off + (uint32_t)(i * b_step * 128),
+                                        in ? pool + (size_t)(block_rank0(u) + j) * p.NC + n0 + b_c * 8 : p.B, in ? 16 : 0);
+                    } else {  // a row of A_a, eight ranks; what lies past the rank is not a number
+                        const int j = (b_c & 1) * 8, live = n0 + row < p.NC ? min(8, max(0, block_live(u) - j)) : 0;
+                        ptx::cp_async16(buf + b_off + (uint32_t)(i * b_step * 64),
+                                        live ? pool + (size_t)(n0 + row) * p.r_max + block_rank0(u) + j : p.B, 2 * live);
                     }
                 }
+                ptx::cp_async_commit();
+            };
+            const uint32_t bufs = base_u + (uint32_t)(p.stages * p.stage_bytes);
+            const int ahead = p.lbufs - 1;  // steps copied beyond the one handed over
+            uint32_t lb = 0, turn = 0, hb = 0;  // the next step's buffer and its turns; the next to hand over
+            int held = 0;                       // steps copied and not handed over
+            auto hand_over = [&]() {
+                ptx::fence_proxy_async_smem();
+                ptx::named_sync(2, kGBuilders);
+                if (bt == 0) {
+                    if (PAIR) ptx::mbar_arrive_remote(leaders(&lfull[hb]));
+                    else ptx::mbar_arrive(&lfull[hb]);
+                }
+                if (++hb == (uint32_t)p.lbufs) hb = 0;
+                --held;
             };
             bool more = advance();
-            if (more) {
-                blocks_of_step();
-                load();
-            }
-            for (uint32_t step = 0; more; ++step) {
-                const uint32_t lb = p.lbufs == 2 ? step & 1 : 0, turn = p.lbufs == 2 ? step >> 1 : step;
-                const int last = MODE == kGBwd ? block_live(ub[0]) - (b_c & 1) * 8 : 8;  // ranks of the pieces of A_a that count
-                more = advance();
-                if (more) blocks_of_step();
+            if (more) blocks_of_step();
+            while (more) {
                 if (turn > 0 && !wait_role(1, kGBuilders, bt == 0, &lempty[lb], (turn - 1) & 1, abort_flag, status, kGStBuild,
                                            p.timeout_ns))
                     break;
-                uint8_t *sa = bufs + lb * p.lora_bytes + a_off, *sb = bufs + lb * p.lora_bytes + b_off;
-#pragma unroll
-                for (int i = 0; i < kGMaxA; ++i)
-                    if (a_row + i * a_step < a_rows) *reinterpret_cast<uint4*>(sa + i * a_step * 128) = ra[i];
-#pragma unroll
-                for (int i = 0; i < kGMaxB; ++i) {
-                    if (MODE == kGBwd && last < 8) {  // what lies past the rank is not a number
-                        uint32_t* w = reinterpret_cast<uint32_t*>(&rb[i]);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) w[h] &= last > 2 * h + 1 ? 0xffffffffu : (last > 2 * h ? 0xffffu : 0u);
-                    }
-                    if (b_row + i * b_step < b_rows)
-                        *reinterpret_cast<uint4*>(sb + i * b_step * (MODE == kGFwd ? 128 : 64)) = rb[i];
+                copy(bufs + lb * (uint32_t)p.lora_bytes);
+                if (++lb == (uint32_t)p.lbufs) {
+                    lb = 0;
+                    ++turn;
                 }
-                ptx::fence_proxy_async_smem();
-                if (more) load();  // in flight over the barrier and the next wait
-                ptx::named_sync(2, kGBuilders);
-                if (bt == 0) {
-                    if (PAIR) ptx::mbar_arrive_remote(leaders(&lfull[lb]));
-                    else ptx::mbar_arrive(&lfull[lb]);
+                more = advance();
+                if (more) blocks_of_step();
+                if (++held > ahead) {
+                    if (ahead == 0) ptx::cp_async_wait<0>();
+                    else ptx::cp_async_wait<1>();
+                    hand_over();
                 }
             }
+            ptx::cp_async_wait<0>();
+            while (held > 0) hand_over();  // (after an abort nobody reads them)
         }
     } else {
         // ================================================================ drain
@@ -833,6 +840,14 @@ operand_kernel(const OperandParams p)
     if (tid == 0) p.list_len[m] = total;
 }
 
+// LoRA step buffers beside a ring of enough stages (36 tokens of 32 adapters: one 56 us, two or three 48).
+int lora_buffers(const GatedParams& p, int room, bool pair)
+{
+    int n = 1;
+    while (n < kGMaxLora && room - (n + 1) * p.lora_bytes >= (pair ? 5 : 4) * p.stage_bytes) ++n;
+    return n;
+}
+
 template <int MODE, bool LORA, bool PAIR>
 cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int grid, cudaStream_t stream)
 {
@@ -1032,7 +1047,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         const int half = p.cols / (plan.pair ? 2 : 1);
         p.lora_bytes = (int)lora_b_offset(p) + (bwd ? half * 64 : (half + 63) / 64 * p.ups * 2048);
         p.lora_bytes = (p.lora_bytes + 1023) / 1024 * 1024;
-        p.lbufs = room - 2 * p.lora_bytes >= 4 * p.stage_bytes ? 2 : 1;
+        p.lbufs = lora_buffers(p, room, plan.pair);
         room -= p.lbufs * p.lora_bytes;
     }
     p.stages = room / p.stage_bytes;

@@ -143,6 +143,7 @@ struct OuterSide {
 struct OuterParams {
     OuterSide a, b;  // dA, dB
     int a_blocks;    // CTAs of dA along the grid's x, then those of dB
+    int run;         // blocks of 64 l that a CTA does one after the other
     const int32_t* perm;
     const int32_t* indptr;
     const int32_t* ranks;
@@ -173,97 +174,171 @@ gated_outer_kernel(const OuterParams p)
     ptx::pdl_launch_dependents();
     const bool long_rows = (int)blockIdx.x < p.a_blocks;
     const OuterSide& d = long_rows ? p.a : p.b;
-    const int l0 = ((int)blockIdx.x - (long_rows ? 0 : p.a_blocks)) * kOL, a = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int lb0 = ((int)blockIdx.x - (long_rows ? 0 : p.a_blocks)) * p.run, a = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int blocks = min(p.run, (d.L + kOL - 1) / kOL - lb0);
     const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
     const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
     const uint16_t* lng = d.lng + (size_t)s * d.lng_slice;
     const uint16_t* ops = d.ops + (size_t)s * p.M * (2 * R16);
     const uint32_t base = ptx::smem_u32(smem);
     const int steps = (n_tok + T - 1) / T;
-
-    auto fetch = [&](int step) {
-        if (step < steps) {
-            const uint32_t st = base + (uint32_t)((step % kOStages) * kStage);
-#pragma unroll
-            for (int i = 0; i < T * (kOL / 8) / kOThreads; ++i) {
-                const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * T + t;
-                const bool in = pos < n_tok && l0 + c * 8 < d.L;
-                const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * d.L + l0 + c * 8 : lng;
-                ptx::cp_async16(st + o_chunk<8>(t, c), src, in ? 16 : 0);
-            }
-#pragma unroll
-            for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
-                const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * T + t;
-                const bool in = pos < n_tok;
-                const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
-                ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
-            }
-        }
-        ptx::cp_async_commit();
-    };
+    const int i8 = lane >> 3, rr = lane & 7;
 
     float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    for (int k = 0; k < kOStages - 1; ++k) fetch(k);
-    for (int step = 0; step < steps; ++step) {
-        ptx::cp_async_wait<kOStages - 2>();
-        __syncthreads();  // the step's rows are here, and the previous step's are consumed
-        fetch(step + kOStages - 1);
-        const uint32_t st = base + (uint32_t)((step % kOStages) * kStage), so = st + kLngBytes;
-        const int i = lane >> 3, rr = lane & 7;
-#pragma unroll
-        for (int ks = 0; ks < T / 16; ++ks) {
-            uint32_t A[4];
-            ptx::ldsm_x4_t(st + o_chunk<8>(ks * 16 + (i >> 1) * 8 + rr, warp * 2 + (i & 1)), A[0], A[1], A[2], A[3]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t b[4];
-                    ptx::ldsm_x4_t(so + o_chunk<kOpCh>(ks * 16 + (i & 1) * 8 + rr, h * NT + n + (i >> 1)), b[0], b[1], b[2],
-                                   b[3]);
-                    ptx::mma_bf16_16816(acc[n], A, b[0], b[1]);
-                    ptx::mma_bf16_16816(acc[n + 1], A, b[2], b[3]);
-                }
-        }
-    }
-    ptx::cp_async_wait<0>();
-    // one rounding to the adapters' type; columns past the rank are zero
-    const int g = lane >> 2, q = lane & 3;
-    if (long_rows) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int j = n * 8 + q * 2;
-            if (j >= p.r_max) continue;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int l = l0 + warp * 16 + g + h * 8;
-                if (l < d.L)
-                    *reinterpret_cast<uint32_t*>(d.out + (((size_t)s * p.n_adapters + a) * d.L + l) * p.r_max + j) =
-                        pack_bf16x2(j < r ? acc[n][2 * h] : 0.f, j + 1 < r ? acc[n][2 * h + 1] : 0.f);
-            }
-        }
-    } else {
-        __syncthreads();
-        uint16_t* o = reinterpret_cast<uint16_t*>(smem);  // [R16][64], 8 elements of padding per row
-        constexpr int kPitch = kOL + 8;
+    auto clear = [&]() {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = n * 8 + q * 2 + (e & 1), l = warp * 16 + g + (e >> 1) * 8;
-                o[j * kPitch + l] = (uint16_t)(pack_bf16x2(j < r ? acc[n][e] : 0.f, 0.f) & 0xffffu);
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    };
+    // The block's 64 x r_max values, rounded once to the adapters' type (past the rank zero), through
+    // shared memory to whole 16-byte pieces of the gradient.
+    auto finish = [&](int l0) {
+        uint16_t* o = reinterpret_cast<uint16_t*>(smem + kOStages * kStage);
+        const int g = lane >> 2, q = lane & 3;
+        constexpr int kPitchA = R16 + 8, kPitchB = kOL + 8;
+        __syncthreads();  // the previous block's values are out
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int j = n * 8 + q * 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int l = warp * 16 + g + h * 8;
+                const uint32_t v = pack_bf16x2(j < r ? acc[n][2 * h] : 0.f, j + 1 < r ? acc[n][2 * h + 1] : 0.f);
+                if (long_rows) {
+                    *reinterpret_cast<uint32_t*>(o + l * kPitchA + j) = v;
+                } else {
+                    o[j * kPitchB + l] = (uint16_t)(v & 0xffffu);
+                    o[(j + 1) * kPitchB + l] = (uint16_t)(v >> 16);
+                }
             }
-        __syncthreads();
-        for (int idx = tid; idx < p.r_max * (kOL / 8); idx += kOThreads) {
-            const int j = idx >> 3, c = idx & 7, l = l0 + c * 8;
-            if (l < d.L)
-                *reinterpret_cast<uint4*>(d.out + (((size_t)s * p.n_adapters + a) * p.r_max + j) * d.L + l) =
-                    *reinterpret_cast<const uint4*>(o + j * kPitch + c * 8);
         }
+        __syncthreads();
+        if (long_rows) {  // [64][r_max], one run of memory
+            const int pieces = p.r_max >> 3, lg = __ffs(pieces) - 1;
+            uint16_t* out = d.out + (((size_t)s * p.n_adapters + a) * d.L + l0) * p.r_max;
+            for (int idx = tid; idx < kOL * pieces; idx += kOThreads) {
+                const int l = idx >> lg, c = idx & (pieces - 1);
+                if (l0 + l < d.L) *reinterpret_cast<uint4*>(out + idx * 8) = *reinterpret_cast<const uint4*>(o + l * kPitchA + c * 8);
+            }
+        } else {
+            for (int idx = tid; idx < p.r_max * (kOL / 8); idx += kOThreads) {
+                const int j = idx >> 3, c = idx & 7, l = l0 + c * 8;
+                if (l < d.L)
+                    *reinterpret_cast<uint4*>(d.out + (((size_t)s * p.n_adapters + a) * p.r_max + j) * d.L + l) =
+                        *reinterpret_cast<const uint4*>(o + j * kPitchB + c * 8);
+            }
+        }
+    };
+
+    if (steps <= 1) {
+        // All tokens in one step: the operands stay in registers, the blocks' rows stream by.
+        const uint16_t* rows[T * 8 / kOThreads];
+#pragma unroll
+        for (int i = 0; i < T * 8 / kOThreads; ++i) {
+            const int t = (tid >> 3) + i * (kOThreads / 8);
+            rows[i] = t < n_tok ? lng + (size_t)p.perm[t0 + t] * d.L + (tid & 7) * 8 : nullptr;
+        }
+        auto fetch = [&](int b) {
+            if (b < blocks) {
+                const uint32_t st = base + (uint32_t)((b % kOStages) * kStage);
+                const int l0 = (lb0 + b) * kOL;
+#pragma unroll
+                for (int i = 0; i < T * 8 / kOThreads; ++i) {
+                    const bool in = rows[i] && l0 + (tid & 7) * 8 < d.L;
+                    ptx::cp_async16(st + o_chunk<8>((tid >> 3) + i * (kOThreads / 8), tid & 7), in ? rows[i] + l0 : lng, in ? 16 : 0);
+                }
+            }
+            ptx::cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
+            const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh;
+            const bool in = t < n_tok;
+            const uint16_t* src = in ? ops + (size_t)p.perm[t0 + t] * (2 * R16) + c * 8 : ops;
+            ptx::cp_async16(base + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
+        }
+        for (int k = 0; k < kOStages - 1; ++k) fetch(k);
+        uint32_t bf[T / 16][2][NT][2];
+        for (int b = 0; b < blocks; ++b) {
+            ptx::cp_async_wait<kOStages - 2>();
+            __syncthreads();  // the block's rows are here, and the previous one's are consumed
+            fetch(b + kOStages - 1);
+            if (b == 0)
+#pragma unroll
+                for (int ks = 0; ks < T / 16; ++ks)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < NT; n += 2)
+                            ptx::ldsm_x4_t(base + kLngBytes + o_chunk<kOpCh>(ks * 16 + (i8 & 1) * 8 + rr, h * NT + n + (i8 >> 1)),
+                                           bf[ks][h][n][0], bf[ks][h][n][1], bf[ks][h][n + 1][0], bf[ks][h][n + 1][1]);
+            clear();
+            const uint32_t st = base + (uint32_t)((b % kOStages) * kStage);
+#pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks) {
+                if (ks * 16 >= n_tok) break;
+                uint32_t A[4];
+                ptx::ldsm_x4_t(st + o_chunk<8>(ks * 16 + (i8 >> 1) * 8 + rr, warp * 2 + (i8 & 1)), A[0], A[1], A[2], A[3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ptx::mma_bf16_16816(acc[n], A, bf[ks][h][n][0], bf[ks][h][n][1]);
+            }
+            finish((lb0 + b) * kOL);
+        }
+        ptx::cp_async_wait<0>();
+        return;
+    }
+
+    for (int b = 0; b < blocks; ++b) {
+        const int l0 = (lb0 + b) * kOL;
+        auto fetch = [&](int step) {
+            if (step < steps) {
+                const uint32_t st = base + (uint32_t)((step % kOStages) * kStage);
+#pragma unroll
+                for (int i = 0; i < T * (kOL / 8) / kOThreads; ++i) {
+                    const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * T + t;
+                    const bool in = pos < n_tok && l0 + c * 8 < d.L;
+                    const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * d.L + l0 + c * 8 : lng;
+                    ptx::cp_async16(st + o_chunk<8>(t, c), src, in ? 16 : 0);
+                }
+#pragma unroll
+                for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
+                    const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * T + t;
+                    const bool in = pos < n_tok;
+                    const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
+                    ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
+                }
+            }
+            ptx::cp_async_commit();
+        };
+        __syncthreads();  // the previous block's rows are consumed
+        clear();
+        for (int k = 0; k < kOStages - 1; ++k) fetch(k);
+        for (int step = 0; step < steps; ++step) {
+            ptx::cp_async_wait<kOStages - 2>();
+            __syncthreads();  // the step's rows are here, and the previous step's are consumed
+            fetch(step + kOStages - 1);
+            const uint32_t st = base + (uint32_t)((step % kOStages) * kStage), so = st + kLngBytes;
+#pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks) {
+                uint32_t A[4];
+                ptx::ldsm_x4_t(st + o_chunk<8>(ks * 16 + (i8 >> 1) * 8 + rr, warp * 2 + (i8 & 1)), A[0], A[1], A[2], A[3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t f[4];
+                        ptx::ldsm_x4_t(so + o_chunk<kOpCh>(ks * 16 + (i8 & 1) * 8 + rr, h * NT + n + (i8 >> 1)), f[0], f[1], f[2],
+                                       f[3]);
+                        ptx::mma_bf16_16816(acc[n], A, f[0], f[1]);
+                        ptx::mma_bf16_16816(acc[n + 1], A, f[2], f[3]);
+                    }
+            }
+        }
+        finish(l0);
+        ptx::cp_async_wait<0>();
     }
 }
 
@@ -477,14 +552,12 @@ cudaError_t launch_shrink(const ShrinkParams& p, int sides, int rows, cudaStream
 template <int R16, int T>
 cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 {
-    size_t smem = (size_t)kOStages * (T * kOL * 2 + T * R16 * 4);
-    const size_t out = (size_t)R16 * (kOL + 8) * 2;  // dB's tile on its way out
-    if (smem < out) smem = out;
+    const size_t smem = (size_t)kOStages * (T * kOL * 2 + T * R16 * 4) + (size_t)(R16 + 8) * (kOL + 8) * 2;
     auto kern = gated_outer_kernel<R16, T>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.a_blocks + (p.b.L + kOL - 1) / kOL), (unsigned)p.n_adapters, 2);
+    cfg.gridDim = dim3((unsigned)(p.a_blocks + ((p.b.L + kOL - 1) / kOL + p.run - 1) / p.run), (unsigned)p.n_adapters, 2);
     cfg.blockDim = dim3(kOThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -496,11 +569,15 @@ cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Few tokens per adapter: short steps, whose buffers let more CTAs run on an SM.
+// Few tokens per adapter: short steps, whose buffers let more CTAs run on an SM, and several blocks per
+// CTA, so that the next block's rows arrive while one is finished.
 template <int R16>
-cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
+cudaError_t launch_outer(OuterParams& p, cudaStream_t stream)
 {
-    return p.M <= 32LL * p.n_adapters ? launch_outer<R16, 32>(p, stream) : launch_outer<R16, 64>(p, stream);
+    const bool few = p.M <= 32LL * p.n_adapters;
+    p.run = few ? 4 : 1;
+    p.a_blocks = ((p.a.L + kOL - 1) / kOL + p.run - 1) / p.run;
+    return few ? launch_outer<R16, 32>(p, stream) : launch_outer<R16, 64>(p, stream);
 }
 
 }  // namespace
@@ -599,7 +676,6 @@ cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const
     p.b.ops = static_cast<const uint16_t*>(ops_v);
     p.b.out = static_cast<uint16_t*>(dB);
     p.b.L = pool.h_out;
-    p.a_blocks = (p.a.L + kOL - 1) / kOL;
     p.perm = seg.perm;
     p.indptr = seg.indptr;
     p.ranks = pool.ranks;
