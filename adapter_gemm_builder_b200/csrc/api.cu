@@ -114,9 +114,10 @@ size_t bwd_ws_layout(int M, const lora_pool_t* pool, size_t* off_at, size_t* off
     return off;
 }
 
-// Gated forward workspace: status | with adapters: planes of v | operands | rank blocks.
+// Gated forward workspace: status | with adapters: planes of v | operands | rank blocks | marks of
+// non-finite adapters.
 struct GatedWs {
-    size_t v, ops, lists, size;
+    size_t v, ops, lists, bad, size;
 };
 GatedWs gated_ws(int M, const lora_pool_t* pool)
 {
@@ -129,13 +130,15 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     w.size += align256(gated_operand_bytes(M, pool->r_max));
     w.lists = w.size;
     w.size += align256(gated_list_bytes(M));
+    w.bad = w.size;
+    w.size += align256(gated_bad_bytes(*pool));
     return w;
 }
 
 // Gated backward workspace: status | counts | parts of shared tiles | dg, du | with adapters:
-// x expanded | planes of u, of v | operands of u, of v | rank blocks.
+// x expanded | planes of u, of v | operands of u, of v | rank blocks | marks of non-finite adapters.
 struct GatedBwdWs {
-    size_t count, part, d, x, u, v, ops_u, ops_v, lists, size;
+    size_t count, part, d, x, u, v, ops_u, ops_v, lists, bad, size;
 };
 GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 {
@@ -158,16 +161,18 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
     w.size += align256(gated_operand_bytes(M, pool->r_max));
     w.lists = w.size;
     w.size += align256(gated_list_bytes(M));
+    w.bad = w.size;
+    w.size += align256(gated_bad_bytes(*pool));
     return w;
 }
 
 // v = x.A (down) or d.B^T of both slices of each side, then its operands and the token tiles' rank blocks.
 cudaError_t gated_operands(const GatedSide* sides, int n, bool backward, bool save, const lora_pool_t& pool,
-                           const lora_segments_t& seg, int M, void* lists, cudaStream_t s)
+                           const lora_segments_t& seg, int M, uint8_t* bad, void* lists, cudaStream_t s)
 {
-    const cudaError_t e = launch_gated_shrink(sides, n, M, pool, seg, s);
+    const cudaError_t e = launch_gated_shrink(sides, n, M, pool, seg, bad, s);
     if (e != cudaSuccess) return e;
-    return launch_gated_operands(sides, n, M, pool, seg, backward, save, lists, s);
+    return launch_gated_operands(sides, n, M, pool, seg, bad, backward, save, lists, s);
 }
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
@@ -659,7 +664,7 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
         const GatedSide side = {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops};
-        if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+        if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
         a.lora = true;
         a.ops = w + l.ops;
         a.lists = w + l.lists;
@@ -717,7 +722,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     }
     const GatedSide sides[2] = {{false, dg, (int64_t)M * F, reinterpret_cast<float*>(w + l.u), w + l.ops_u},
                                 {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops_v}};
-    if (gated_operands(sides, 2, true, false, *pool, *seg, M, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+    if (gated_operands(sides, 2, true, false, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
     a.ops = w + l.ops_u;

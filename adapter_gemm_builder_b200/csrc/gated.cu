@@ -230,11 +230,13 @@ struct Walk {
     // shrink its first quarter
     __device__ __forceinline__ int lora_first() const { return seen == 1 ? k0 + (k1 - k0) / 4 : k0; }
 };
-// A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has.
-__device__ __forceinline__ int block_code(int adapter, int block, int live) { return adapter << 8 | block << 6 | live; }
+// A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has, whether
+// the adapter is marked as non-finite.
+__device__ __forceinline__ int block_code(int adapter, int block, int live, bool bad) { return adapter << 8 | block << 6 | (bad ? 32 : 0) | live; }
 __device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
 __device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
-__device__ __forceinline__ int block_live(int u) { return u & 63; }
+__device__ __forceinline__ int block_live(int u) { return u & 31; }
+__device__ __forceinline__ bool block_bad(int u) { return u & 32; }
 constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
 // LoRA steps of a token tile with this many rank blocks, both slices; a piece of a shared tile has
 // its share of them.
@@ -562,7 +564,26 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             const int ahead = p.lbufs - 1;  // steps copied beyond the one handed over
             uint32_t lb = 0, turn = 0, hb = 0;  // the next step's buffer and its turns; the next to hand over
             int held = 0;                       // steps copied and not handed over
+            uint32_t odd = 0, odd_next = 0;     // of the step to hand over and the one behind: pieces of marked adapters
             auto hand_over = [&]() {
+                if (odd) {  // their non-finite elements become zero (see operand_kernel)
+                    uint8_t* at = smem_raw + (bufs - raw_u) + hb * (uint32_t)p.lora_bytes + b_off;
+#pragma unroll
+                    for (int i = 0; i < kGMaxB; ++i)
+                        if (odd >> i & 1) {
+                            uint4* v = reinterpret_cast<uint4*>(at + i * b_step * (MODE == kGFwd ? 128 : 64));
+                            uint4 w = *v;
+                            uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                if ((e[h] & 0x7f80u) == 0x7f80u) e[h] &= 0xffff0000u;
+                                if ((e[h] & 0x7f800000u) == 0x7f800000u) e[h] &= 0xffffu;
+                            }
+                            *v = w;
+                        }
+                }
+                odd = odd_next;
+                odd_next = 0;
                 ptx::fence_proxy_async_smem();
                 ptx::named_sync(2, kGBuilders);
                 if (bt == 0) {
@@ -579,6 +600,12 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                                            p.timeout_ns))
                     break;
                 copy(bufs + lb * (uint32_t)p.lora_bytes);
+                uint32_t marks = 0;
+#pragma unroll
+                for (int i = 0; i < kGMaxB; ++i)
+                    if (b_row + i * b_step < b_rows && block_bad(MODE == kGFwd ? ub[i] : ub[0])) marks |= 1u << i;
+                if (held == 0) odd = marks;
+                else odd_next = marks;
                 if (++lb == (uint32_t)p.lbufs) {
                     lb = 0;
                     ++turn;
@@ -757,6 +784,8 @@ struct OperandParams {
     const int32_t* ranks;
     const float* scales;
     int M, n_adapters, r_max, r16;
+    const uint8_t* bad;  // [2][n_adapters][kGatedScanMax], bad_parts of them written (a multiple of 4)
+    int bad_parts;
     int tile;  // tokens a list covers: 128 or 256
     int32_t* lists;
     int32_t* list_len;
@@ -764,8 +793,23 @@ struct OperandParams {
 
 constexpr int kOpThreads = 256;
 constexpr int kOpRows = 16;  // tokens per CTA
+constexpr int kPlanesMax = 8;
 
-// s_a v of both slices as bf16 halves hi + lo (columns past the rank zero), and per token tile the rank blocks that its rows use, adapters in order of first appearance.
+// Whether the matrix of adapter a and slice s was marked as non-finite.
+__device__ __forceinline__ bool marked(const OperandParams& p, int a, int s)
+{
+    const uint4* at = reinterpret_cast<const uint4*>(p.bad + ((size_t)s * p.n_adapters + a) * kGatedScanMax);
+    const uint4 v[2] = {at[0], at[1]};
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad = bad || (4 * k < p.bad_parts && w[k]);
+    return bad;
+}
+
+// s_a v of both slices as bf16 halves hi + lo (columns past the rank zero; NaN for an adapter whose
+// matrix is not finite, so that its own tokens show it: the GEMM's copy of the matrix has its
+// non-finite elements zeroed, and the other tokens' zeros stay zeros), and per token tile the rank blocks that its rows use, adapters in order of first appearance.
 // Lets the GEMM start at once (see the wait there).
 __global__ void __launch_bounds__(kOpThreads)
 operand_kernel(const OperandParams p)
@@ -779,22 +823,33 @@ operand_kernel(const OperandParams p)
         const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
         const int row = (int)blockIdx.x * kOpRows + rs % kOpRows;
         if (row >= p.M) continue;
+        // everything that does not wait for the adapter first: the planes (past r_max: none; of a
+        // row without an adapter: whatever is there, not used)
         const int a = p.tok_adapter[row];
+        float4 v[kPlanesMax][2];
+        const float* src = d.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
+#pragma unroll
+        for (int k = 0; k < kPlanesMax; ++k)
+            if (k < d.planes && 8 * c < p.r_max) {
+                v[k][0] = *reinterpret_cast<const float4*>(src + k * p.plane);
+                v[k][1] = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
+            }
         if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
+        const bool bad = blockIdx.y == 0 && marked(p, a, s);
         const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
         const float scale = p.scales ? p.scales[a] : 1.f;
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (8 * c < r) {
-            const float* src = d.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
-            for (int k = 0; k < d.planes; ++k) {
-                const float4 x = *reinterpret_cast<const float4*>(src + k * p.plane);
-                const float4 y = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
-                f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-                f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+#pragma unroll
+        for (int k = 0; k < kPlanesMax; ++k)
+            if (k < d.planes && 8 * c < r) {
+                f[0] += v[k][0].x; f[1] += v[k][0].y; f[2] += v[k][0].z; f[3] += v[k][0].w;
+                f[4] += v[k][1].x; f[5] += v[k][1].y; f[6] += v[k][1].z; f[7] += v[k][1].w;
             }
-        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
+        if (bad)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7fc00000u);
         uint4* o = reinterpret_cast<uint4*>(d.ops + ((size_t)s * p.M + row) * (2 * p.r16));
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -810,7 +865,7 @@ operand_kernel(const OperandParams p)
     }
     const int per = p.tile / kOpRows, m = (int)blockIdx.x / per;
     if (blockIdx.y || (int)blockIdx.x % per) return;  // one CTA of the tile makes its list
-    __shared__ int s_id[kOpThreads];
+    __shared__ __align__(16) int s_id[kOpThreads];
     __shared__ int s_cnt[kOpThreads / 32];
     const int row = m * p.tile + tid;
     int id = tid < p.tile && row < p.M ? p.tok_adapter[row] : -1;
@@ -818,7 +873,11 @@ operand_kernel(const OperandParams p)
     s_id[tid] = id;
     __syncthreads();
     bool first = id >= 0;
-    for (int j = 0; j < tid; ++j) first = first && s_id[j] != id;
+    for (int j = 0; j < (tid & ~3); j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(s_id + j);
+        first = first && o.x != id && o.y != id && o.z != id && o.w != id;
+    }
+    for (int j = tid & ~3; j < tid; ++j) first = first && s_id[j] != id;
     // rank blocks before this thread's, by a scan over the tile
     const int rank = first ? max(1, min(p.ranks ? p.ranks[id] : p.r_max, p.r_max)) : 0, mine = (rank + 15) / 16;
     int at = mine;
@@ -836,7 +895,8 @@ operand_kernel(const OperandParams p)
         total += s_cnt[w];
     }
     int32_t* list = p.lists + (size_t)m * kListMax * (p.tile / kGTileM);
-    for (int b = 0; b < mine; ++b) list[at + b] = block_code(id, b, min(16, rank - 16 * b));
+    const bool bad = first && (marked(p, id, 0) || marked(p, id, 1));
+    for (int b = 0; b < mine; ++b) list[at + b] = block_code(id, b, min(16, rank - 16 * b), bad);
     if (tid == 0) p.list_len[m] = total;
 }
 
@@ -974,7 +1034,7 @@ size_t gated_list_bytes(int M)
 }
 
 cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                  bool backward, bool save, void* lists, cudaStream_t stream)
+                                  const uint8_t* bad, bool backward, bool save, void* lists, cudaStream_t stream)
 {
     const GatedPlan plan = gated_plan(backward, M, pool.h_in, pool.h_out, save);
     OperandParams p = {};
@@ -985,6 +1045,8 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
         p.side[i].ops = static_cast<uint16_t*>(sides[i].ops);
     }
     p.plane = (long long)pool.n_slices * M * pool.r_max;
+    p.bad = bad;
+    p.bad_parts = gated_scan_parts(sides[0].down, M, pool);
     p.tok_adapter = seg.tok_adapter;
     p.ranks = pool.ranks;
     p.scales = pool.scales;

@@ -360,12 +360,53 @@ struct ShrinkSide {
     int L, planes, steps;  // steps of 64 per plane
     bool down;
 };
+constexpr int kScanPer = 4;  // scanning CTAs per plane
+static_assert(8 * kScanPer <= kGatedScanMax, "marks of a scan's parts");
 struct ShrinkParams {
     ShrinkSide side[2];
+    int sides;
     const int32_t* perm;
+    const int32_t* indptr;
     const int4* tiles;
+    const int32_t* ranks;
     int M, n_adapters, r_max;
+    // the pool's matrices that the GEMM multiplies with (forward B, backward A)
+    const uint16_t* scan;
+    bool scan_rows;   // their rows are ranks (B)
+    int scan_L, scan_parts;
+    uint8_t* bad;     // [2][n_adapters][kGatedScanMax]
 };
+
+// Whether adapter a's matrix of slice s holds a non-finite value in part `part` of its live elements.
+// The GEMM multiplies every row of a token tile with it, most by zero, and zero times infinity would
+// carry one tenant's broken adapter into another's tokens; a marked one is kept out of them
+// (operand_kernel). The pass also brings the matrices into L2 for the GEMM.
+__device__ __forceinline__ void scan_adapter(const ShrinkParams& p, int a, int s, int part)
+{
+    const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
+    const uint4* m = reinterpret_cast<const uint4*>(p.scan + ((size_t)s * p.n_adapters + a) * p.r_max * p.scan_L);
+    const int per_row = p.r_max >> 3;  // 16-byte pieces of a row of A
+    const long long all = p.scan_rows ? (long long)r * (p.scan_L >> 3) : (long long)p.scan_L * per_row;
+    const long long i0 = all * part / p.scan_parts, i1 = all * (part + 1) / p.scan_parts;
+    bool odd = false;
+    constexpr int kAhead = 8;
+    for (long long i = i0 + threadIdx.x; i < i1; i += kAhead * kOThreads) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k] = i + k * kOThreads < i1 ? m[i + k * kOThreads] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            // elements of this piece that count: rows of A end at the rank
+            const int live = p.scan_rows ? 8 : r - (int)((i + k * kOThreads) & (per_row - 1)) * 8;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                odd = odd || (2 * e < live && (w[e] & 0x7f80u) == 0x7f80u) || (2 * e + 1 < live && (w[e] & 0x7f800000u) == 0x7f800000u);
+        }
+    }
+    odd = __syncthreads_or(odd);
+    if (threadIdx.x == 0) p.bad[((size_t)s * p.n_adapters + a) * kGatedScanMax + part] = odd;
+}
 
 // R16 ranks; DOWN: the rows of w are l.
 template <bool DOWN, int R16>
@@ -455,7 +496,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const ShrinkS
     }
 }
 
-// Grid: tile rows x planes x (side, slice).
+// Grid: tile rows x planes x (side or scan, slice).
 template <int R16>
 __global__ void __launch_bounds__(kOThreads)
 gated_shrink_kernel(const ShrinkParams p)
@@ -463,6 +504,14 @@ gated_shrink_kernel(const ShrinkParams p)
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
+    const int scan = (int)(blockIdx.z >> 1) - p.sides;
+    if (scan >= 0) {  // an adapter's first tile scans its matrix
+        const int4 tl = p.tiles[blockIdx.x];
+        const int planes = p.side[0].planes;
+        if (tl.x >= 0 && tl.x < p.n_adapters && tl.z > 0 && p.indptr[tl.x] == tl.y && (int)blockIdx.y < planes)
+            scan_adapter(p, tl.x, (int)blockIdx.z & 1, scan * planes + (int)blockIdx.y);
+        return;
+    }
     const ShrinkSide& d = p.side[blockIdx.z >> 1];
     if ((int)blockIdx.y >= d.planes) return;
     if (d.down) shrink_tile<true, R16>(p, d, smem);
@@ -480,10 +529,14 @@ gated_shrink_token_kernel(const ShrinkParams p, const int32_t* __restrict__ tok_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    const int t = (int)blockIdx.x, plane = (int)blockIdx.y, s = (int)blockIdx.z;
+    const int t = (int)blockIdx.x, plane = (int)blockIdx.y, s = (int)blockIdx.z & 1;
     const ShrinkSide& d = p.side[0];
     const int a = tok_adapter[t];
     if (a < 0 || a >= p.n_adapters) return;
+    if (blockIdx.z >= 2) {  // an adapter's first token scans its matrix
+        if (p.perm[p.indptr[a]] == t) scan_adapter(p, a, s, ((int)(blockIdx.z >> 1) - 1) * (int)gridDim.y + plane);
+        return;
+    }
     const uint16_t* x = d.lng + (size_t)s * d.lng_slice + (size_t)t * d.L;
     const uint16_t* w = d.w + ((size_t)s * p.n_adapters + a) * p.r_max * d.L;
     const int pieces = p.r_max >> 3, c = tid & (pieces - 1), step = kOThreads / pieces;
@@ -537,7 +590,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, int sides, int rows, cudaStream
     if (e != cudaSuccess) return e;
     const int planes = sides == 2 && p.side[1].planes > p.side[0].planes ? p.side[1].planes : p.side[0].planes;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows, (unsigned)planes, (unsigned)(2 * sides));
+    cfg.gridDim = dim3((unsigned)rows, (unsigned)planes, (unsigned)(2 * sides + 2 * kScanPer));
     cfg.blockDim = dim3(kOThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -625,10 +678,24 @@ int gated_shrink_planes(int M, int L, int n_adapters)
     return (int)(planes < 1 ? 1 : (planes > 8 ? 8 : planes));
 }
 
+int gated_scan_parts(bool down, int M, const lora_pool_t& pool)
+{
+    return kScanPer * gated_shrink_planes(M, down ? pool.h_in : pool.h_out, pool.n_adapters);
+}
+size_t gated_bad_bytes(const lora_pool_t& pool) { return (size_t)2 * pool.n_adapters * kGatedScanMax; }
+
 cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                cudaStream_t stream)
+                                uint8_t* bad, cudaStream_t stream)
 {
     ShrinkParams p = {};
+    p.sides = n;
+    p.scan_rows = sides[0].down;
+    p.scan = static_cast<const uint16_t*>(p.scan_rows ? pool.B : pool.A);
+    p.scan_L = p.scan_rows ? pool.h_out : pool.h_in;
+    p.scan_parts = gated_scan_parts(sides[0].down, M, pool);
+    p.bad = bad;
+    p.indptr = seg.indptr;
+    p.ranks = pool.ranks;
     for (int i = 0; i < n; ++i) {
         ShrinkSide& d = p.side[i];
         d.down = sides[i].down;
@@ -647,7 +714,7 @@ cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora
     p.r_max = pool.r_max;
     if (n == 1 && sides[0].down && tile_tokens_for(M, pool.n_adapters) <= LORA_DECODE_TILE_TOKENS) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)M, (unsigned)p.side[0].planes, 2);
+        cfg.gridDim = dim3((unsigned)M, (unsigned)p.side[0].planes, 2 + 2 * kScanPer);
         cfg.blockDim = dim3(kOThreads, 1, 1);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];

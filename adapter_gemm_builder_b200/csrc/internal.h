@@ -87,14 +87,19 @@ struct GatedSide {
     void* ops;  // where launch_gated_operands puts the side's operands
 };
 int gated_shrink_planes(int M, int L, int n_adapters);
+// Also marks the adapters whose matrix in the GEMM to come (forward B, backward A) holds a
+// non-finite value: bad[slice][adapter][part], gated_scan_parts parts (gated_bad_bytes).
+constexpr int kGatedScanMax = 32;
+int gated_scan_parts(bool down, int M, const lora_pool_t& pool);
+size_t gated_bad_bytes(const lora_pool_t& pool);
 cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                cudaStream_t stream);
+                                uint8_t* bad, cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
 size_t gated_part_bytes();
 size_t gated_count_bytes();
 cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                  bool backward, bool save, void* lists, cudaStream_t stream);
+                                  const uint8_t* bad, bool backward, bool save, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
     bool backward;
     int M, K, F, act;

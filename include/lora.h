@@ -472,11 +472,14 @@ LORA_API int act8_expand_rows(const lora_act8_t* in, int M, int N, void* x, lora
  *   pool: NULL, or n_slices == 2 (slice 0 the gate's adapters, slice 1 up's), h_in == K,
  *   h_out == F. seg: required when pool != NULL (built for these M tokens).
  *   ws: lora_workspace_size(LORA_OP_BF16_GATED, M, K, pool) bytes.
- * With adapters: the shrink (v = x.A, fp32), a small kernel that lists each 128-token tile's
+ * With adapters: the shrink (v = x.A, fp32), a small kernel that lists each token tile's
  * adapters and puts s_a v into bf16 halves hi + lo, then the GEMM as its programmatic
  * dependent; the term is part of the GEMM's sum. Its cost grows with the adapters per
- * 128 consecutive tokens, so batches sorted by adapter cost least. Results do not depend on
- * other tokens of the batch.
+ * 128 consecutive tokens, so batches sorted by adapter cost least. An adapter whose B (forward) or
+ * A (backward) holds a non-finite value gives NaN to the whole rows of its own tokens (and to
+ * its dA), and nothing to those of others.
+ * h, g8 and u8 overlap neither each other nor an input; calls that may run at the same time have
+ * a workspace each.
  * Limits: M >= 1, K % 8 == 0, F % 8 == 0, F % 16 == 0 with checkpoints.
  */
 LORA_API int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void* Wg, const void* Wu, int act,
@@ -498,7 +501,8 @@ LORA_API int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, c
  *   x8 needs K % 16 == 0); dA bf16 [2][n_adapters][K][r_max], dB bf16 [2][n_adapters][r_max][F].
  *   With pool == NULL, x, x8, dA and dB are not used (NULL).
  *   ws: lora_workspace_size(LORA_OP_BF16_GATED_BACKWARD, M, F, pool) bytes (K there is the
- *   backward's reduction size, F).
+ *   backward's reduction size, F). Outputs overlap neither each other nor an input; calls that
+ *   may run at the same time have a workspace each.
  * Limits: M >= 1, K % 8 == 0, F % 16 == 0.
  */
 LORA_API int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* dh, int M, int K, int F,

@@ -347,7 +347,6 @@ def test_other_stream_bad_ids_and_repeat():
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     h, _ = forward(p, stream=s)
-    p2_ids = p.ids.copy()
     p.ids[p.ids == 9] = -1
     check_forward(p, "silu", h)
     h2, _ = forward(p)
@@ -365,10 +364,103 @@ def test_non_finite_rows_stay_in_their_rows():
     assert not torch.isfinite(dirty[3]).any()
 
 
-def test_wait_runs_out_then_next_call_is_correct():
+@pytest.mark.parametrize("M,K,F,r", [(40, 256, 512, 16), (200, 128, 304, 8), (700, 136, 9504, 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_broken_adapter_stays_with_its_tokens(M, K, F, r, value):
+    """One adapter's B (forward) or A (backward) holds an infinity or NaN: the rows of its tokens are NaN,
+    the other rows, and the other adapters' gradients, are bit for bit what they are without it."""
+    p = Problem(M, K, F, 4, r, "uniform", seed=11, ranks=[r, max(1, r - 3), r, 1])
+    mine = torch.from_numpy(p.ids == 1)
+    clean, kept = forward(p, save=True)
+    o = backward(p)
+    A, B = p.A.clone(), p.B.clone()
+    p.B[1, 1, 0, F // 2] = value
+    dirty, bad = forward(p, save=True)
+    assert torch.equal(clean[~mine], dirty[~mine]) and torch.isnan(dirty[mine]).all()
+    other = (~mine).cuda()
+    for a, b in zip(kept, bad):
+        assert torch.equal(a.codes[other], b.codes[other]) and torch.equal(a.scales[other], b.scales[other])
+    p.B, p.A = B, A
+    p.A[0, 1, K // 2, 0] = value
+    d = backward(p)
+    assert torch.equal(o["dX"][other], d["dX"][other]) and torch.isnan(d["dX"][mine.cuda()]).all()
+    for g in ("dA", "dB"):
+        for a in (0, 2, 3):
+            assert torch.equal(o[g][:, a], d[g][:, a])
+
+
+def test_captured_as_the_very_first_call():
+    """In a process of its own: nothing ran before the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from adapter_gemm_builder_b200 import lora as L
+M, K, F = 600, 96, 9616
+bf = dict(dtype=torch.bfloat16, device="cuda")
+x, Wg, Wu, h = torch.randn(M, K, **bf), torch.randn(F, K, **bf), torch.randn(F, K, **bf), torch.empty(M, F, **bf)
+dh, dX = torch.randn(M, F, **bf), torch.empty(M, K, **bf)
+g8, u8 = L.Act8(M, F), L.Act8(M, F)
+wf, wb = L.workspace(L.LORA_OP_BF16_GATED, M, K, None), L.workspace(L.LORA_OP_BF16_GATED_BACKWARD, M, F, None)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    L.bf16_gated_gemm_lora_epilogue(x, Wg, Wu, None, None, h, wf, save=(g8, u8))
+    L.bf16_gated_lora_backward(dh, Wg, Wu, None, None, g8, u8, None, dX, None, None, wb)
+g.replay()
+torch.cuda.synchronize()
+a, b = h.clone(), dX.clone()
+L.bf16_gated_gemm_lora_epilogue(x, Wg, Wu, None, None, h, wf, save=(g8, u8))
+L.bf16_gated_lora_backward(dh, Wg, Wu, None, None, g8, u8, None, dX, None, None, wb)
+torch.cuda.synchronize()
+assert torch.equal(a, h) and torch.equal(b, dX)
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=180)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_graphs_with_a_workspace_each_on_two_streams():
+    """Two captured calls replayed at the same time, each with its own workspace."""
+    p = Problem(150, 256, 1040, 5, 16, "uniform", seed=12)
+    pool, seg = p.device()
+    x, Wg, Wu = p.x.cuda(), p.Wg.cuda(), p.Wu.cuda()
+    want, _ = forward(p)
+    runs = []
+    for _ in range(2):
+        h = torch.zeros(150, 1040, dtype=torch.bfloat16, device="cuda")
+        ws = L.workspace(L.LORA_OP_BF16_GATED, 150, 256, pool)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            L.bf16_gated_gemm_lora_epilogue(x, Wg, Wu, pool, seg, h, ws)
+        runs.append((g, h, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, _, _, s in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, h, ws, _ in runs:
+        assert L.lora_workspace_status(ws)[0] == L.LORA_OK
+        assert torch.equal(h.cpu().double(), want)
+
+
+def test_backward_twice_gives_the_same_bits():
+    """Shared tiles are finished by whichever piece is done last, the sum is the same."""
+    p = Problem(180, 512, 6000, 3, 16, "uniform", seed=13)
+    a = backward(p)
+    for _ in range(5):
+        b = backward(p)
+        for k in ("dX", "dA", "dB"):
+            assert torch.equal(a[k], b[k]), k
+
+
+@pytest.mark.parametrize("M,K,F", [(300, 256, 512), (700, 136, 9496)])  # single CTAs, pairs
+def test_wait_runs_out_then_next_call_is_correct(M, K, F):
     """The bounded wait: a stalled launch returns and reports it, the next call is right."""
     for n in (0, 3):
-        p = Problem(300, 256, 512, n, 16, "uniform", seed=8)
+        p = Problem(M, K, F, n, 16, "uniform", seed=8)
         pool, seg = p.device()
         h = torch.empty(p.M, p.F, dtype=torch.bfloat16, device="cuda")
         ws = L.workspace(L.LORA_OP_BF16_GATED, p.M, p.K, pool)
