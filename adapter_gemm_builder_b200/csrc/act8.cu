@@ -23,7 +23,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kLaneCols = 16;
 constexpr int kTaskCols = 32 * kLaneCols;
 constexpr int kInFlight = 2;
-constexpr int kCtasPerSm = 8;
 
 __device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7fff7fffu; }
 
@@ -190,10 +189,13 @@ act8_expand_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict_
 template <typename... P, typename... A>
 cudaError_t launch_tasks(void (*kern)(P...), uint32_t tasks, cudaStream_t stream, A... args)
 {
-    const uint32_t most = (uint32_t)device_sm_count() * kCtasPerSm;
-    const uint32_t need = (tasks + kWarps - 1) / kWarps;
+    // a warp per task while that fills the SMs once, then kInFlight tasks per warp: many small CTAs
+    // end more evenly than a grid of resident ones walking the rest (30.7 -> 28 us for the pair at
+    // 2704 x 11008)
+    const uint32_t one = (tasks + kWarps - 1) / kWarps, all = (one + kInFlight - 1) / kInFlight;
+    const uint32_t fill = (uint32_t)device_sm_count() * 4;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(need < most ? need : most, 1, 1);
+    cfg.gridDim = dim3(one < fill ? one : (all < fill ? fill : all), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

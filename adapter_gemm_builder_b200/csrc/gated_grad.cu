@@ -26,7 +26,6 @@ constexpr int kEThreads = 256;
 constexpr int kEWarps = kEThreads / 32;
 constexpr int kETaskCols = 256;
 constexpr int kEInFlight = 2;
-constexpr int kECtasPerSm = 6;
 
 struct PointParams {
     const uint16_t* dh;
@@ -652,9 +651,10 @@ cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora
     p.F = F;
     p.segs = (uint32_t)((F + kETaskCols - 1) / kETaskCols);
     p.tasks = (uint32_t)M * p.segs;
-    const uint32_t most = (uint32_t)device_sm_count() * kECtasPerSm, need = (p.tasks + kEWarps - 1) / kEWarps;
+    const uint32_t one = (p.tasks + kEWarps - 1) / kEWarps, all = (one + kEInFlight - 1) / kEInFlight;
+    const uint32_t fill = (uint32_t)device_sm_count() * 4;  // as in act8.cu
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(need < most ? need : most, 1, 1);
+    cfg.gridDim = dim3(one < fill ? one : (all < fill ? fill : all), 1, 1);
     cfg.blockDim = dim3(kEThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -399,10 +399,15 @@ def _act8(a: "Act8 | None", shape, what: str, device=None):
     return a._ref
 
 
+# the handle of a device's current stream without the Stream object around it (2 us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(device, stream, name: str, *args):
     """One library call with `device` current, on the stream (the device's current one by default)."""
     f = getattr(_lib or load(), name)
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    s = _raw_stream(device.index) if stream is None else stream.cuda_stream
     if device.index == torch.cuda.current_device():
         status = f(*args, s)
     else:
