@@ -19,8 +19,9 @@
 // into bf16 halves hi + lo that add up in the accumulator (16 bits of v). The steps have shared
 // memory of their own beside the ring and are spread between the main stages (in a CTA's first
 // tile from its second quarter on, so that the shrink runs under the first); the builders copy
-// with cp.async, one step ahead of the one that they hand over where two buffers fit. (Steps in ring slots, loaded when the slot was free,
-// had cost the ring about 2 us each: 36 tokens of 32 adapters took 160 us, 37 us without them.)
+// with cp.async, one step ahead of the one that they hand over where two buffers fit. (Steps in ring
+// slots, loaded when the slot was free, had cost the ring about 2 us each: 36 tokens of 32 adapters
+// took 160 us, 37 us without them; now 53.)
 // Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
 // are sorted by adapter has few adapters per tile.
 //
