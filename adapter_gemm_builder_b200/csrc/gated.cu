@@ -70,7 +70,7 @@ constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 12;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
 constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the one CTA per SM (1 KB is static)
-constexpr int kGSmemShort = 208 * 1024;       // the same with fewer than 128 tokens
+constexpr int kGSmemShort = 208 * 1024;       // the same with at most 64 tokens
 constexpr int kGBarBytes = 512;
 constexpr int kGMaxLora = 2;                  // LoRA step buffers
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
@@ -980,6 +980,7 @@ constexpr TileChoice kFwdTiles[] = {{true, 128, .373}, {true, 96, .309}, {true, 
 constexpr int kFwdSaveTiles = 7;  // with checkpoints: whole blocks of 32 columns
 constexpr TileChoice kBwdTiles[] = {{true, 256, .42}, {true, 128, .357}, {false, 256, .45}, {false, 128, .38}, {false, 64, .336}};
 constexpr double kShareUs = 40;  // what pieces have to gain: accumulators go out and in, the tail is longer
+constexpr double kPieceUs = 1.2;  // and each more of a tile
 constexpr int kMaxSplit = 16, kPieces = 3;  // pieces of a tile; of all tiles per unit, at most
 
 // The cheapest choice: rounds of the units over the tiles, whole or with the last one shared. A
@@ -991,6 +992,7 @@ GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
     const TileChoice* tiles = bwd ? kBwdTiles : kFwdTiles;
     const int n = bwd ? (int)(sizeof(kBwdTiles) / sizeof(TileChoice)) : (save ? kFwdSaveTiles : (int)(sizeof(kFwdTiles) / sizeof(TileChoice)));
     const int pairs = M > kGTileM ? pair_count() : 0, sms = device_sm_count();
+    const double weights = 4. * K * F / 6.5e6;  // their stream at 6.5 TB/s: no sharing beats it
     GatedPlan best = {};
     double least = 0;
     for (int i = 0; i < n; ++i) {
@@ -1005,7 +1007,8 @@ GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
             if (split > 1 && (!bwd || rem == 0 || rem * split > (long long)kPieces * units || red < 8 * split))
                 break;
             const double last = (double)((rem * split + units - 1) / units) / split;
-            const double t = ((double)(all / units) + last) * us + (split > 1 ? kShareUs : 0);
+            double t = ((double)(all / units) + last) * us;
+            if (split > 1) t = (t < weights ? weights : t) + kShareUs + split * kPieceUs;
             if (best.cols && t >= least) continue;
             least = t;
             best.pair = c.pair;
@@ -1097,12 +1100,11 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     p.a_bytes = a_rows * 128;
     p.b_bytes = p.bn * 128 / (plan.pair ? 2 : 1);
     p.stage_bytes = p.a_bytes + p.b_bytes;
-    // Full token tiles take all shared memory. Fewer tokens leave some of it, so that the small
-    // kernels before this one keep running beside its CTAs (which then start at once, the
-    // weights streaming under the shrink); their 16 KB at the end are what the MMA may read past a
-    // short operand tile.
-    int room = (a_rows < kGTileM ? kGSmemShort - kGTileM * 128 : kGSmem) - kGBarBytes - 1024;
-    p.smem = a_rows < kGTileM ? kGSmemShort : kGSmem;
+    // Many tokens take all shared memory. Few leave some of it, so that the small kernels before this
+    // one keep running beside its CTAs (which then start at once, the weights streaming under the
+    // shrink). At the end: what the MMA may read past a short operand tile.
+    p.smem = a_rows > kGTileM / 2 ? kGSmem : kGSmemShort;
+    int room = p.smem - (kGTileM - a_rows) * 128 - kGBarBytes - 1024;
     if (a.lora) {
         p.r16 = (a.r_max + 15) / 16 * 16;
         // rank blocks per step: what four pieces per builder and the space beside four stages hold

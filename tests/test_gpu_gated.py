@@ -389,6 +389,43 @@ def test_a_broken_adapter_stays_with_its_tokens(M, K, F, r, value):
             assert torch.equal(o[g][:, a], d[g][:, a])
 
 
+def test_more_than_four_billion_elements():
+    """Offsets past 32 bits: the last rows of 2^18 tokens by F 16400, forward with checkpoints and backward."""
+    M, K, F, n, r = 1 << 18, 64, 16400, 2, 8
+    p = Problem(150, K, F, n, r, "uniform", seed=14, none_frac=0.0)
+    pool, _ = p.device()
+    tail = p.M
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    ids[-tail:] = torch.from_numpy(p.ids).cuda()
+    seg = L.Segments(M, n)
+    L.lora_build_segments(ids, n, seg)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, h = torch.zeros(M, K, **bf), torch.empty(M, F, **bf)
+    x[-tail:] = p.x.cuda()
+    Wg, Wu = p.Wg.cuda(), p.Wu.cuda()
+    g8, u8 = L.Act8(M, F), L.Act8(M, F)
+    ws = L.workspace(L.LORA_OP_BF16_GATED, M, K, pool)
+    L.bf16_gated_gemm_lora_epilogue(x, Wg, Wu, pool, seg, h, ws, save=(g8, u8))
+    torch.cuda.synchronize()
+    assert L.lora_workspace_status(ws)[0] == L.LORA_OK
+    check_forward(p, "silu", h[-tail:].cpu().double())
+    assert not h[:-tail:997].any()
+    values = []
+    for k in (g8, u8):
+        v = torch.empty(tail, F, **bf)
+        L.act8_expand_rows(L.Act8.of(k.codes[-tail:], k.scales[-tail:]), v)
+        values.append(v.cpu().double())
+    dh = h.zero_()  # its buffer again
+    dh[-tail:] = p.dh.cuda()
+    dX, dA, dB = torch.empty(M, K, **bf), torch.empty_like(pool.A), torch.empty_like(pool.B)
+    ws = L.workspace(L.LORA_OP_BF16_GATED_BACKWARD, M, F, pool)
+    L.bf16_gated_lora_backward(dh, Wg, Wu, pool, seg, g8, u8, x, dX, dA, dB, ws)
+    torch.cuda.synchronize()
+    assert L.lora_workspace_status(ws)[0] == L.LORA_OK
+    assert not dX[:-tail:997].any()
+    check_backward(p, "silu", dict(g=values[0], u=values[1], x=p.x.double(), dX=dX[-tail:], dA=dA, dB=dB, h=None))
+
+
 def test_captured_as_the_very_first_call():
     """In a process of its own: nothing ran before the capture."""
     import os
