@@ -979,19 +979,27 @@ constexpr TileChoice kFwdTiles[] = {{true, 128, .373}, {true, 96, .309}, {true, 
                                     {false, 80, .304}, {false, 48, .30}, {false, 16, .30}};
 constexpr int kFwdSaveTiles = 7;  // with checkpoints: whole blocks of 32 columns
 constexpr TileChoice kBwdTiles[] = {{true, 256, .42}, {true, 128, .357}, {false, 256, .45}, {false, 128, .38}, {false, 64, .336}};
+// What a single CTA's tile costs above that next to a pair's. A row pitch off 128 bytes makes each
+// row of a load straddle two lines, and a pair loads half as much of B per CTA (2048 x 7624 x 5056
+// forward: pairs 275 us, single CTAs 332; backward 512 x 1024 x 5216: 39 and 52). On aligned rows
+// the pair is ahead where the table calls it even (937 x 6144 x 9952: 165 us, 174).
+constexpr double kSingleCost = 1.03, kSingleSplitRows = 1.3;
 constexpr double kShareUs = 40;  // what pieces have to gain: accumulators go out and in, the tail is longer
 constexpr double kPieceUs = 1.2;  // and each more of a tile
 constexpr int kMaxSplit = 16, kPieces = 3;  // pieces of a tile; of all tiles per unit, at most
 
 // The cheapest choice: rounds of the units over the tiles, whole or with the last one shared. A
 // single token tile is bound by the weights' stream instead: there time per stage goes by bytes
-// (8192 x 28672, 16 tokens: 112 columns in two rounds 6.4 TB/s, 16 columns in thirteen 2 TB/s).
+// (8192 x 28672, 16 tokens: 112 columns in two rounds 6.4 TB/s, 16 columns in thirteen 2 TB/s). A
+// pair's one tile is 256 tokens and half as many pairs share the stream (200 x 7424 x 8640: pairs,
+// which read the weights once, 53 us, single CTAs 61).
 GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
 {
     const int NC = bwd ? K : F, red = bwd ? 2 * ((F + 63) / 64) : (K + 63) / 64;
     const TileChoice* tiles = bwd ? kBwdTiles : kFwdTiles;
     const int n = bwd ? (int)(sizeof(kBwdTiles) / sizeof(TileChoice)) : (save ? kFwdSaveTiles : (int)(sizeof(kFwdTiles) / sizeof(TileChoice)));
     const int pairs = M > kGTileM ? pair_count() : 0, sms = device_sm_count();
+    const double single = K % 64 || (bwd && F % 64) ? kSingleSplitRows : kSingleCost;
     const double weights = 4. * K * F / 6.5e6;  // their stream at 6.5 TB/s: no sharing beats it
     GatedPlan best = {};
     double least = 0;
@@ -1001,7 +1009,8 @@ GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
         if (units < 1) continue;
         const int mt = (M + (c.pair ? 255 : 127)) / (c.pair ? 256 : 128);
         const long long all = (long long)mt * ((NC + c.cols - 1) / c.cols);
-        const double stream = (bwd ? .0028 : .0055) * c.cols, us = red * (mt == 1 && stream > c.us ? stream : c.us);
+        const double stream = (bwd ? .0028 : .0055) * c.cols / (c.pair ? 2 : 1), work = c.pair || !pairs ? c.us : c.us * single;
+        const double us = red * (mt == 1 && stream > work ? stream : work);
         const long long rem = all % units;
         for (int split = 1; split <= kMaxSplit; ++split) {
             if (split > 1 && (!bwd || rem == 0 || rem * split > (long long)kPieces * units || red < 8 * split))
