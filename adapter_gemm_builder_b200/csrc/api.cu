@@ -115,9 +115,9 @@ size_t bwd_ws_layout(int M, const lora_pool_t* pool, size_t* off_at, size_t* off
 }
 
 // Gated forward workspace: status | with adapters: planes of v | operands | rank blocks | marks of
-// non-finite adapters.
+// non-finite adapters | rows of x by adapter.
 struct GatedWs {
-    size_t v, ops, lists, bad, size;
+    size_t v, ops, lists, bad, rows, size;
 };
 GatedWs gated_ws(int M, const lora_pool_t* pool)
 {
@@ -132,6 +132,8 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     w.size += align256(gated_list_bytes(M));
     w.bad = w.size;
     w.size += align256(gated_bad_bytes(*pool));
+    w.rows = w.size;
+    w.size += align256(gated_gather_bytes(M, pool->h_in));
     return w;
 }
 
@@ -664,12 +666,15 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
         const GatedSide side = {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops};
+        if (launch_gated_gather(x, M, *pool, *seg, g8 != nullptr, w + l.rows, s) != cudaSuccess) return LORA_ERR_CUDA;
         if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
         a.lora = true;
+        a.a[1] = w + l.rows;
         a.ops = w + l.ops;
         a.lists = w + l.lists;
         a.B = pool->B;
         a.tok_adapter = seg->tok_adapter;
+        a.order = seg->perm;
         a.n_adapters = pool->n_adapters;
         a.r_max = pool->r_max;
     }

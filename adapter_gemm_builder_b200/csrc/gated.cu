@@ -22,8 +22,14 @@
 // with cp.async, one step ahead of the one that they hand over where two buffers fit. (Steps in ring
 // slots, loaded when the slot was free, had cost the ring about 2 us each: 36 tokens of 32 adapters
 // took 160 us, 37 us without them; now 53.)
-// Tokens stay in the caller's order: no gather of x, no scatter of h; a batch whose tokens
-// are sorted by adapter has few adapters per tile.
+// The forward takes the tokens of more than one token tile in the segments' order, by adapter: a tile
+// then needs few adapters' blocks however the batch is mixed. gather_kernel copies x's rows into that
+// order, except where 128 of them follow one another already, as in a batch that comes sorted; h
+// and the checkpoints are written to the tokens' own rows. (2048 tokens mixed over 48 adapters of
+// rank 16: 940 us in their own order, 298 in this; over 16 of rank 64 1480, 336. TMA's gather of four
+// rows at a time took 1.2 us a stage instead of .4.)
+// The backward keeps the caller's order: its sums are long beside its steps (mixed 463 us,
+// sorted 407; 672 and 551).
 //
 // More than 128 tokens usually run on pairs of CTAs (cta_group::2, clusters of two): 256 tokens by
 // the same columns, each CTA with its 128 rows of A and half of B (forward: the even CTA the
@@ -105,6 +111,7 @@ struct GatedParams {
     const int32_t* lists;     // [mt][kListMax per 128 tokens] rank blocks of a token tile (see block_code)
     const int32_t* list_len;  // [mt]
     const int32_t* tok_adapter;
+    const int32_t* order;     // the token of each row of the tiles (NULL: the rows are the tokens)
     int n_adapters, r_max, r16;
     int ups;                  // rank blocks per step
     int lbufs, lora_bytes;    // step buffers behind the ring
@@ -254,6 +261,26 @@ __device__ __forceinline__ uint64_t g_desc_k64(uint32_t a)
            ((uint64_t)4 << 61);
 }
 
+// A warp's look at the 128 rows of a tile from row0 on, in the segments' order: are their tokens a run?
+// Then the rows are read where they are, else from the copy that gather_kernel made.
+struct RowRun {
+    int tok[4];
+    __device__ __forceinline__ void load(const int32_t* order, int M, int row0, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tok[i] = order[min(row0 + lane * 4 + i, M - 1)];
+    }
+    // the first token, or -1: no run
+    __device__ __forceinline__ int first(int M, int row0, int lane) const
+    {
+        const int t0 = __shfl_sync(0xffffffffu, tok[0], 0);
+        bool run = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) run = run && (row0 + lane * 4 + i >= M || tok[i] == t0 + lane * 4 + i);
+        return __all_sync(0xffffffffu, run) ? t0 : -1;
+    }
+};
+
 template <int MODE, bool LORA, bool PAIR>
 __global__ void __launch_bounds__(kGThreads, 1)
 gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
@@ -335,15 +362,28 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
             else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
         };
+        // where a tile's rows of x are (see RowRun), of the next tile's a tile ahead
+        constexpr bool kOrder = MODE == kGFwd && LORA;
+        RowRun run, next_run;
+        if (kOrder && p.order && unit < p.tiles) next_run.load(p.order, p.M, (unit % p.mt) * kTokens + rank * kGTileM, lane);
         for (Walk w(unit); ok && w.next(p);) {
-            const int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM, n0 = (w.tile / p.mt) * p.cols;
+            int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM, n0 = (w.tile / p.mt) * p.cols;
+            bool copied = false;
+            if (kOrder && p.order) {
+                run = next_run;
+                const int t0 = run.first(p.M, row0, lane);
+                copied = t0 < 0;
+                if (!copied) row0 = t0;
+                const int after = w.tile + p.units;
+                if (after < p.tiles) next_run.load(p.order, p.M, (after % p.mt) * kTokens + rank * kGTileM, lane);
+            }
             for (int kb = w.k0; kb < w.k1; ++kb) {
                 if (use > 0 && !(ok = wait_warp(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns))) break;
                 const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
                 if (leader) {
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(kCtas * (p.a_bytes + p.b_bytes)));
                     if (MODE == kGFwd) {
-                        load(sa, &tmA0, kb * kGKBlock, row0);
+                        load(sa, kOrder && copied ? &tmA1 : &tmA0, kb * kGKBlock, row0);
                         if (PAIR) {
                             load(sb, rank ? &tmB1 : &tmB0, kb * kGKBlock, n0);
                         } else {
@@ -515,7 +555,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < kGMaxA; ++i) {
                         const int row = a_row + i * a_step, tok = row0 + row;
-                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
+                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[MODE == kGFwd && p.order ? p.order[tok] : tok] : -2;
                     }
                 }
                 return true;
@@ -630,6 +670,8 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         for (Walk w(unit); w.next(p); ++acc) {
             const int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM + q * 32, n0 = (w.tile / p.mt) * p.cols, buf = acc & 1;
             const int row = row0 + lane;
+            // the row's place in the outputs
+            const int out_row = MODE == kGFwd && LORA && p.order && row < p.M ? p.order[row] : row;
             if (!wait_role(3, kGDrainWarps * 32, threadIdx.x == 0, &tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status,
                            kGStDrain, p.timeout_ns))
                 break;
@@ -702,7 +744,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         ptx::tmem_ld32(ta + (uint32_t)(p.cols + c), u);
                         if (row < p.M) {
                             const int live = min(32, p.NC - col);
-                            const size_t at = (size_t)row * p.NC + col, sc = (size_t)row * nb + (col >> 5);
+                            const size_t at = (size_t)out_row * p.NC + col, sc = (size_t)out_row * nb + (col >> 5);
                             save_block(g, live, p.g_codes + at, p.g_scales + sc);
                             save_block(u, live, p.u_codes + at, p.u_scales + sc);
 #pragma unroll
@@ -727,7 +769,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             ptx::tmem_ld32(ta + (uint32_t)c, g);
                         }
                         if (row < p.M) {
-                            uint16_t* o = p.out + (size_t)row * p.NC + col;
+                            uint16_t* o = p.out + (size_t)out_row * p.NC + col;
 #pragma unroll
                             for (int i = 0; i < kN; i += 8)
                                 if (col + i < p.NC) store_bf16x8(o + i, g + i);
@@ -772,6 +814,33 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     }
 }
 
+// ------------------------------------------------------------------ tokens by adapter
+//
+// Rows of x in the segments' order, for the tiles that RowRun calls copied (the GEMM decides the same
+// way). A CTA copies kGatherRows rows of 2048 columns, all of them in flight.
+
+constexpr int kGatherThreads = 256, kGatherRows = 16, kGatherCols = kGatherThreads * 8;
+
+__global__ void __launch_bounds__(kGatherThreads)
+gather_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ order, int M, int K, uint16_t* __restrict__ out)
+{
+    ptx::pdl_launch_dependents();  // the shrink waits for this kernel to be complete
+    ptx::pdl_wait();
+    const int row0 = (int)blockIdx.x * kGatherRows, lane = threadIdx.x & 31;
+    RowRun run;
+    run.load(order, M, row0 / kGTileM * kGTileM, lane);
+    if (run.first(M, row0 / kGTileM * kGTileM, lane) >= 0) return;
+    const int col = (int)blockIdx.y * kGatherCols + (int)threadIdx.x * 8;
+    if (col >= K) return;
+    uint4 v[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+        if (row0 + i < M) v[i] = *reinterpret_cast<const uint4*>(x + (size_t)order[row0 + i] * K + col);
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+        if (row0 + i < M) *reinterpret_cast<uint4*>(out + (size_t)(row0 + i) * K + col) = v[i];
+}
+
 // ------------------------------------------------------------------ LoRA operands
 
 struct OperandParams {
@@ -782,6 +851,7 @@ struct OperandParams {
     } side[2];           // blockIdx.y; the lists are made with the first
     long long plane;
     const int32_t* tok_adapter;
+    const int32_t* order;  // as the GEMM's
     const int32_t* ranks;
     const float* scales;
     int M, n_adapters, r_max, r16;
@@ -826,9 +896,9 @@ operand_kernel(const OperandParams p)
         if (row >= p.M) continue;
         // everything that does not wait for the adapter first: the planes (past r_max: none; of a
         // row without an adapter: whatever is there, not used)
-        const int a = p.tok_adapter[row];
+        const int tok = p.order ? p.order[row] : row, a = p.tok_adapter[tok];
         float4 v[kPlanesMax][2];
-        const float* src = d.v + ((size_t)s * p.M + row) * p.r_max + 8 * c;
+        const float* src = d.v + ((size_t)s * p.M + tok) * p.r_max + 8 * c;
 #pragma unroll
         for (int k = 0; k < kPlanesMax; ++k)
             if (k < d.planes && 8 * c < p.r_max) {
@@ -869,7 +939,7 @@ operand_kernel(const OperandParams p)
     __shared__ __align__(16) int s_id[kOpThreads];
     __shared__ int s_cnt[kOpThreads / 32];
     const int row = m * p.tile + tid;
-    int id = tid < p.tile && row < p.M ? p.tok_adapter[row] : -1;
+    int id = tid < p.tile && row < p.M ? p.tok_adapter[p.order ? p.order[row] : row] : -1;
     if (id >= p.n_adapters) id = -1;
     s_id[tid] = id;
     __syncthreads();
@@ -965,6 +1035,16 @@ struct GatedPlan {
     int split;  // pieces of the last round's tiles, 1: they stay whole
 };
 
+// Whether the GEMM takes its tokens by adapter: where it saves a unit six rank blocks or more, if the
+// batch is mixed. (The launch costs a sorted batch 1 us and the copy a mixed one 4: 300 tokens of 5
+// adapters, three blocks saved, 30 us without, 34 with; 1024 tokens, seven saved, 66 and 58.)
+bool gated_order(const GatedPlan& plan, bool bwd, int M, int n_adapters, int r_max)
+{
+    if (bwd || plan.mt < 2) return false;
+    const int R = (r_max + 15) / 16, all = (n_adapters < M ? n_adapters : M) * R;
+    return (double)(all - (double)all / plan.mt - R) * plan.tiles / plan.units >= 6;
+}
+
 // A choice of tile: output columns, and the microseconds a CTA or pair takes per stage (64 of K)
 // with all of them at work, measured on 2048 tokens, 4096 x 11008. Pairs gain by their deeper ring;
 // narrow tiles read their operands from shared memory more often per product, and below 64
@@ -1046,6 +1126,25 @@ size_t gated_list_bytes(int M)
     return (size_t)(M + 2 * kGTileM - 1) / (2 * kGTileM) * 2 * (kListMax + 1) * 4;
 }
 
+size_t gated_gather_bytes(int M, int K) { return M > kGTileM ? (size_t)M * K * 2 : 0; }
+
+cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
+                                cudaStream_t stream)
+{
+    const int K = pool.h_in;
+    if (!gated_order(gated_plan(false, M, K, pool.h_out, save), false, M, pool.n_adapters, pool.r_max)) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((M + kGatherRows - 1) / kGatherRows), (unsigned)((K + kGatherCols - 1) / kGatherCols), 1);
+    cfg.blockDim = dim3(kGatherThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gather_kernel, static_cast<const uint16_t*>(x), (const int32_t*)seg.perm, M, K, static_cast<uint16_t*>(out));
+}
+
 cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
                                   const uint8_t* bad, bool backward, bool save, void* lists, cudaStream_t stream)
 {
@@ -1061,6 +1160,7 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     p.bad = bad;
     p.bad_parts = gated_scan_parts(sides[0].down, M, pool);
     p.tok_adapter = seg.tok_adapter;
+    if (gated_order(plan, backward, M, pool.n_adapters, pool.r_max)) p.order = seg.perm;
     p.ranks = pool.ranks;
     p.scales = pool.scales;
     p.M = M;
@@ -1143,6 +1243,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.lists = static_cast<const int32_t*>(a.lists);
         p.list_len = p.lists + (size_t)p.mt * kListMax * (plan.pair ? 2 : 1);
         p.tok_adapter = a.tok_adapter;
+        if (gated_order(plan, bwd, a.M, a.n_adapters, a.r_max)) p.order = a.order;
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
     }
@@ -1151,7 +1252,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     bool ok = true;
     for (int i = 0; i < 2; ++i) {
-        ok = ok && encode_tmap_2d(&tm[i], dt, bwd ? a.a[i] : a.a[0], (uint64_t)red, (uint64_t)a.M, (uint64_t)red * 2,
+        ok = ok && encode_tmap_2d(&tm[i], dt, bwd || p.order ? a.a[i] : a.a[0], (uint64_t)red, (uint64_t)a.M, (uint64_t)red * 2,
                                   kGKBlock, (uint32_t)a_rows, sw);
         ok = ok && encode_tmap_2d(&tm[2 + i], dt, a.W[i], (uint64_t)a.K, (uint64_t)a.F, (uint64_t)a.K * 2, kGKBlock,
                                   bwd ? kGKBlock : (uint32_t)p.cols, sw);

@@ -94,6 +94,10 @@ int gated_scan_parts(bool down, int M, const lora_pool_t& pool);
 size_t gated_bad_bytes(const lora_pool_t& pool);
 cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
                                 uint8_t* bad, cudaStream_t stream);
+// Forward: the rows of x that the GEMM reads in the segments' order (gated.cu), before the shrink.
+size_t gated_gather_bytes(int M, int K);
+cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
+                                cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_list_bytes(int M);
 size_t gated_part_bytes();
@@ -103,7 +107,7 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
 struct GatedGemmArgs {
     bool backward;
     int M, K, F, act;
-    const void* a[2];       // forward: x in a[0]; backward: dg, du [M][F]
+    const void* a[2];       // forward: x, with adapters launch_gated_gather's rows; backward: dg, du [M][F]
     const void* W[2];       // Wg, Wu [F][K]
     void* out;              // h [M][F]; backward: dX [M][K]
     const lora_act8_t* g8;  // forward: both or neither
@@ -115,7 +119,7 @@ struct GatedGemmArgs {
     const void* ops;
     const void* lists;
     const void* B;          // the pool's B, backward: its A
-    const int32_t* tok_adapter;
+    const int32_t *tok_adapter, *order;  // the segments' tok_adapter and perm
     int n_adapters, r_max;
 };
 // cudaErrorInvalidValue if an operand's tensor map is refused.

@@ -141,7 +141,9 @@ def test_forward(M, K, F, n, r, ids, act):
 @pytest.mark.parametrize("M,K,F,n,r,ids", [(1, 64, 16, 0, 8, "uniform"), (5, 128, 48, 2, 8, "uniform"),
                                            (130, 256, 1040, 5, 16, "zipf"), (513, 200, 272, 3, 64, "sorted_zipf"),
                                            (256, 64, 4112, 2, 32, "identical"), (600, 96, 9616, 4, 64, "sorted_zipf"),
-                                           (400, 4096, 1200, 3, 32, "zipf")])
+                                           (400, 4096, 1200, 3, 32, "zipf"),
+                                           # mixed over many adapters: rows copied by adapter
+                                           (700, 136, 9504, 40, 16, "uniform"), (1030, 72, 4112, 130, 32, "zipf")])
 def test_forward_with_checkpoints(M, K, F, n, r, ids):
     """h as without them; a block's scale is the rule's for a largest element within the error of the
     sum, and an element is within half an E4M3 step (2^-4, or half the smallest step) of g or u."""
@@ -351,6 +353,19 @@ def test_other_stream_bad_ids_and_repeat():
     check_forward(p, "silu", h)
     h2, _ = forward(p)
     assert torch.equal(h, h2)
+
+
+@pytest.mark.parametrize("M,K,F,n,r", [(1000, 136, 9496, 40, 16), (641, 264, 7000, 100, 8)])
+def test_runs_of_tokens_in_any_order(M, K, F, n, r):
+    """Requests one after the other, adapters in no order: some tiles' tokens are a run, others are gathered
+    from everywhere, and tokens without an adapter lie between them."""
+    rng = np.random.default_rng(M)
+    ids = np.repeat(rng.integers(-1, n, 40), rng.integers(1, 60, 40)).astype(np.int32)
+    ids = np.concatenate([np.full(300, n - 1, np.int32), ids, rng.integers(-1, n, M).astype(np.int32)])[:M]
+    p = Problem(M, K, F, n, r, ids, seed=8)
+    h, _ = forward(p)
+    check_forward(p, "silu", h)
+    assert torch.equal(h, forward(p)[0])
 
 
 def test_non_finite_rows_stay_in_their_rows():
