@@ -127,7 +127,7 @@ GatedWs gated_ws(int M, const lora_pool_t* pool)
     w.v = w.size;
     w.size += align256(apply_v_bytes(M, *pool, gated_shrink_planes(M, pool->h_in, pool->n_adapters)));
     w.ops = w.size;
-    w.size += align256(gated_operand_bytes(M, pool->r_max));
+    w.size += align256(gated_expand_bytes(M, pool->n_adapters, pool->r_max));
     w.lists = w.size;
     w.size += align256(gated_list_bytes(M));
     w.bad = w.size;

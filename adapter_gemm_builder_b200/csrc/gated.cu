@@ -72,6 +72,7 @@ constexpr int kGProducer = kGDrainWarps, kGMma = kGProducer + 1, kGBuilder0 = kG
 constexpr int kGBuilders = 256;
 constexpr int kGMaxA = 4, kGMaxB = 4;        // 16-byte pieces of a LoRA step per builder
 constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
+constexpr int kGFwdThreads = kGBuilder0 * 32;  // the forward has no builders
 constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 12;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
@@ -79,6 +80,7 @@ constexpr int kGSmem = 226 * 1024;            // dynamic shared memory of the on
 constexpr int kGSmemShort = 208 * 1024;       // the same with at most 64 tokens
 constexpr int kGBarBytes = 512;
 constexpr int kGMaxLora = 2;                  // LoRA step buffers
+constexpr int kRankBoxes = 5;                // maps of B's rows, boxes of 1, 2, 4, 8 and 16
 constexpr int kGAccCols = 256;                // TMEM columns of an accumulator
 constexpr int kGCounts = 256;                 // counts of shared tiles (fewer than units, two CTAs each)
 constexpr int kListMax = kGTileM * (LORA_MAX_RANK / 16);  // rank blocks of 128 tokens
@@ -106,15 +108,21 @@ struct GatedParams {
     unsigned long long timeout_ns;
     int inject_stall;
     // LoRA
-    const uint16_t* ops;      // [2][M][hi r16 | lo r16]: s_a v as bf16 halves
-    const uint16_t* B;        // forward B [2][n_adapters][r_max][NC], backward A [2][n_adapters][NC][r_max]
+    const uint16_t* ops;      // backward: [2][M][hi r16 | lo r16]: s_a v as bf16 halves
+    const uint16_t* B;        // backward: A [2][n_adapters][NC][r_max]
     const int32_t* lists;     // [mt][kListMax per 128 tokens] rank blocks of a token tile (see block_code)
     const int32_t* list_len;  // [mt]
+    const int32_t* list_base; // forward: the tile's first step in the expanded operand, per slice
     const int32_t* tok_adapter;
     const int32_t* order;     // the token of each row of the tiles (NULL: the rows are the tokens)
     int n_adapters, r_max, r16;
     int ups;                  // rank blocks per step
-    int lbufs, lora_bytes;    // step buffers behind the ring
+    int lbufs, lora_bytes;    // backward: step buffers behind the ring
+};
+struct GatedMaps {
+    CUtensorMap a[2], b[2];     // x and its rows by adapter, or dg, du; Wg, Wu
+    CUtensorMap e;              // forward: the expanded operand (expand_kernel)
+    CUtensorMap l[kRankBoxes];  // forward: the pool's B [2 n_adapters][r_max][NC]
 };
 
 // K-major operand, 128-byte rows, 128-byte swizzle: 8-row groups 1024 bytes apart.
@@ -234,26 +242,47 @@ struct Walk {
         k1 = (int)((long long)p.kb * (piece + 1) / p.split);
         return true;
     }
-    // the stage after which the tile's LoRA steps begin to be spread: a unit's first piece leaves the
-    // shrink its first quarter
-    __device__ __forceinline__ int lora_first() const { return seen == 1 ? k0 + (k1 - k0) / 4 : k0; }
+    // The stage after which the tile's LoRA steps begin to be spread: a unit's first piece leaves the
+    // shrink time. (The forward's steps are stages like others, so they may all come in the last
+    // eighth; the backward's take their time each.)
+    __device__ __forceinline__ int lora_first(bool fwd) const { return seen == 1 ? k0 + (k1 - k0) * (fwd ? 7 : 2) / 8 : k0; }
 };
-// A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has, whether
-// the adapter is marked as non-finite.
-__device__ __forceinline__ int block_code(int adapter, int block, int live, bool bad) { return adapter << 8 | block << 6 | (bad ? 32 : 0) | live; }
-__device__ __forceinline__ int block_adapter(int u) { return u >> 8; }
-__device__ __forceinline__ int block_rank0(int u) { return (u >> 6 & 3) * 16; }
+// A rank block as the lists hold it: adapter, which 16 of its ranks, how many of them it has, the
+// slices whose matrix is marked as non-finite (bits).
+__device__ __forceinline__ int block_code(int adapter, int block, int live, int bad) { return adapter << 9 | block << 7 | bad << 5 | live; }
+__device__ __forceinline__ int block_adapter(int u) { return u >> 9; }
+__device__ __forceinline__ int block_rank0(int u) { return (u >> 7 & 3) * 16; }
 __device__ __forceinline__ int block_live(int u) { return u & 31; }
-__device__ __forceinline__ bool block_bad(int u) { return u & 32; }
-constexpr int kNoBlock = -3 * 256;  // an adapter that no row has, nothing live
+__device__ __forceinline__ int block_bad(int u) { return u >> 5 & 3; }
+constexpr int kNoBlock = -3 * 512;  // an adapter that no row has, nothing live
 // LoRA steps of a token tile with this many rank blocks, both slices; a piece of a shared tile has
 // its share of them.
 __device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
 __device__ __forceinline__ int steps_begin(const GatedParams& p, int steps, int piece) { return piece < 0 ? 0 : steps * piece / p.split; }
 __device__ __forceinline__ int steps_end(const GatedParams& p, int steps, int piece) { return piece < 0 ? steps : steps * (piece + 1) / p.split; }
-// Where a step's B part begins: behind the operand's tiles of 64 columns (four groups of 16:
-// ups of hi, ups of lo).
+// A step's operand: tiles of 64 columns (four groups of 16: ups of hi, ups of lo), the B part behind
+// them.
 __host__ __device__ __forceinline__ uint32_t lora_b_offset(const GatedParams& p) { return (uint32_t)(p.ups / 2 * p.a_bytes); }
+// A tile in the order in which every role takes it: main stages [k0, k1), and between them from
+// lora_first on, evenly, the LoRA steps [e, e + due) that `begin` names. False: given up.
+template <typename Main, typename Begin, typename Step>
+__device__ __forceinline__ bool walk_tile(const Walk& w, bool fwd, Main main_stages, Begin begin, Step step)
+{
+    const int first = w.lora_first(fwd), spread = w.k1 - first;
+    int kb = first + 1, e = 0, due = 0;
+    if (!main_stages(w.k0, kb)) return false;
+    begin(e, due);
+    const int ext = due;
+    for (;;) {
+        for (; due >= spread; due -= spread, ++e)
+            if (!step(e)) return false;
+        if (kb >= w.k1) return true;
+        const int n = ext ? min((spread - due + ext - 1) / ext, w.k1 - kb) : w.k1 - kb;
+        if (!main_stages(kb, kb + n)) return false;
+        kb += n;
+        due += n * ext;
+    }
+}
 // K-major operand of 64-byte rows (32 columns), 64-byte swizzle.
 __device__ __forceinline__ uint64_t g_desc_k64(uint32_t a)
 {
@@ -282,15 +311,16 @@ struct RowRun {
 };
 
 template <int MODE, bool LORA, bool PAIR>
-__global__ void __launch_bounds__(kGThreads, 1)
-gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GatedParams p)
+__global__ void __launch_bounds__(MODE == kGFwd ? kGFwdThreads : kGThreads, 1)
+gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
 {
+    constexpr bool kRing = MODE == kGFwd && LORA;  // LoRA steps come through the ring
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     __shared__ int s_last;       // this CTA's part of a shared tile was the last
-    __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader
+    __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader,
+    __shared__ uint32_t s_tx[kGMaxStages];     // and the bytes of each one's last fill
     constexpr int kCtas = PAIR ? 2 : 1, kTokens = kCtas * kGTileM;
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int unit = (int)blockIdx.x / kCtas;
@@ -362,14 +392,43 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
             else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
         };
+        auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
+            if (PAIR) ptx::tma_load_3d_pair(dst, map, leaders(&full[st]), c0, c1, c2);
+            else ptx::tma_load_3d(dst, map, &full[st], c0, c1, c2);
+        };
+        auto stage_free = [&]() {
+            return ok = use == 0 || wait_warp(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
+        };
+        auto expect = [&](uint32_t bytes) {  // per CTA
+            if (!leader) return;
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[st], kCtas * bytes);
+            if (PAIR) s_tx[st] = bytes;
+        };
+        auto next_stage = [&]() {
+            __syncwarp();
+            if (++st == p.stages) {
+                st = 0;
+                ++use;
+            }
+        };
         // where a tile's rows of x are (see RowRun), of the next tile's a tile ahead
-        constexpr bool kOrder = MODE == kGFwd && LORA;
         RowRun run, next_run;
-        if (kOrder && p.order && unit < p.tiles) next_run.load(p.order, p.M, (unit % p.mt) * kTokens + rank * kGTileM, lane);
+        if (kRing && p.order && unit < p.tiles) next_run.load(p.order, p.M, (unit % p.mt) * kTokens + rank * kGTileM, lane);
+        // the tile's rank blocks, lane l the l-th of 32; the next tile's a tile ahead
+        int blocks = 0, base = 0, codes = 0, next_blocks = 0, next_base = 0, next_codes = 0;
+        auto fetch_list = [&](int tile) {
+            if (tile >= p.tiles) return;
+            const int m = tile % p.mt;
+            next_blocks = p.list_len[m];
+            next_base = p.list_base[m];
+            next_codes = p.lists[(size_t)m * kListMax * kCtas + lane];
+        };
+        bool waited = false;
         for (Walk w(unit); ok && w.next(p);) {
-            int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM, n0 = (w.tile / p.mt) * p.cols;
+            int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM;
+            const int n0 = (w.tile / p.mt) * p.cols;
             bool copied = false;
-            if (kOrder && p.order) {
+            if (kRing && p.order) {
                 run = next_run;
                 const int t0 = run.first(p.M, row0, lane);
                 copied = t0 < 0;
@@ -377,33 +436,86 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                 const int after = w.tile + p.units;
                 if (after < p.tiles) next_run.load(p.order, p.M, (after % p.mt) * kTokens + rank * kGTileM, lane);
             }
-            for (int kb = w.k0; kb < w.k1; ++kb) {
-                if (use > 0 && !(ok = wait_warp(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns))) break;
-                const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
-                if (leader) {
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(kCtas * (p.a_bytes + p.b_bytes)));
-                    if (MODE == kGFwd) {
-                        load(sa, kOrder && copied ? &tmA1 : &tmA0, kb * kGKBlock, row0);
-                        if (PAIR) {
-                            load(sb, rank ? &tmB1 : &tmB0, kb * kGKBlock, n0);
+            auto main_stages = [&](int kb, int stop) {
+                for (; kb < stop; ++kb) {
+                    if (!stage_free()) return false;
+                    const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes), sb = sa + (uint32_t)p.a_bytes;
+                    expect((uint32_t)(p.a_bytes + p.b_bytes));
+                    if (leader) {
+                        if (MODE == kGFwd) {
+                            load(sa, kRing && copied ? &maps.a[1] : &maps.a[0], kb * kGKBlock, row0);
+                            if (PAIR) {
+                                load(sb, &maps.b[rank], kb * kGKBlock, n0);
+                            } else {
+                                load(sb, &maps.b[0], kb * kGKBlock, n0);
+                                load(sb + (uint32_t)(p.cols * 128), &maps.b[1], kb * kGKBlock, n0);
+                            }
                         } else {
-                            load(sb, &tmB0, kb * kGKBlock, n0);
-                            load(sb + (uint32_t)(p.cols * 128), &tmB1, kb * kGKBlock, n0);
+                            const bool up = kb >= p.kb_half;
+                            const int f0 = (up ? kb - p.kb_half : kb) * kGKBlock, c0 = n0 + rank * (p.bn / 2);
+                            load(sa, &maps.a[up], f0, row0);
+                            for (int b = 0; b < p.b_bytes / 8192; ++b)
+                                load(sb + (uint32_t)(b * 8192), &maps.b[up], c0 + b * 64, f0);
                         }
-                    } else {
-                        const bool up = kb >= p.kb_half;
-                        const int f0 = (up ? kb - p.kb_half : kb) * kGKBlock, c0 = n0 + rank * (p.bn / 2);
-                        load(sa, up ? &tmA1 : &tmA0, f0, row0);
-                        for (int b = 0; b < p.b_bytes / 8192; ++b)
-                            load(sb + (uint32_t)(b * 8192), up ? &tmB1 : &tmB0, c0 + b * 64, f0);
+                    }
+                    next_stage();
+                }
+                return true;
+            };
+            if (!kRing) {
+                main_stages(w.k0, w.k1);
+                continue;
+            }
+            auto begin = [&](int& e, int& due) {
+                if (!waited) {
+                    ptx::pdl_wait();
+                    waited = true;
+                    fetch_list(w.tile);
+                }
+                blocks = __shfl_sync(0xffffffffu, next_blocks, 0);
+                base = __shfl_sync(0xffffffffu, next_base, 0);
+                codes = next_codes;
+                fetch_list(w.tile + p.units);
+                e = 0;
+                due = lora_steps(p, blocks);
+            };
+            const int half = p.cols / kCtas;
+            const int rows = PAIR ? kTokens : p.a_bytes >> 7;
+            // this lane's part of a step's B: 64 columns of block k (of four)
+            const int k = lane & 3, atom = lane >> 2, x = n0 + rank * half + atom * 64, atoms = (half + 63) >> 6;
+            const uint32_t b_at = lora_b_offset(p) + (uint32_t)((atom * p.ups + k) * 2048);
+            const int32_t* list = p.lists + (size_t)(w.tile % p.mt) * kListMax * kCtas + lane;
+            auto step = [&](int e) {
+                const int s = e & 1, q = (e >> 1) * p.ups, n = min(p.ups, blocks - q);
+                if (!stage_free()) return false;
+                if (s == 0 && q && (q & 31) == 0) codes = list[q];
+                const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes);
+                expect(lora_b_offset(p) + (uint32_t)(n * atoms * 2048));
+                if (leader)
+                    for (int c = 0; c < p.ups / 2; ++c)
+                        load(sa + (uint32_t)(c * p.a_bytes), &maps.e, 0, ((2 * base + e) * (p.ups / 2) + c) * rows + rank * kGTileM);
+                const int u = __shfl_sync(0xffffffffu, codes, (q + k) & 31);
+                if (k < n && atom < atoms) {
+                    // the block's live rows, then zeros (past the last matrix; a marked one is zeros too,
+                    // see Eight), in boxes of powers of two
+                    const int nothing = 2 * p.n_adapters, live = block_live(u);
+                    int z = block_bad(u) >> s & 1 ? nothing : s * p.n_adapters + block_adapter(u);
+                    for (int row = 0, left = live;;) {
+                        while (left) {
+                            const int b = 31 - __clz(left);
+                            load3(sa + b_at + (uint32_t)(row * 128), &maps.l[b], x, block_rank0(u) + row, z);
+                            row += 1 << b;
+                            left -= 1 << b;
+                        }
+                        if (row == 16) break;
+                        left = 16 - row;
+                        z = nothing;
                     }
                 }
-                __syncwarp();
-                if (++st == p.stages) {
-                    st = 0;
-                    ++use;
-                }
-            }
+                next_stage();
+                return true;
+            };
+            walk_tile(w, MODE == kGFwd, main_stages, begin, step);
         }
         if (PAIR) {  // landed below, once both producers have stopped
             if (lane < p.stages) s_fills[lane] = use + (lane < st ? 1 : 0);
@@ -433,7 +545,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             else ptx::tc_commit(bar);
         };
         // descriptors of stage 0 and of LoRA buffer 0; the address field counts 16-byte units
-        const uint32_t lora_u = base_u + (uint32_t)(p.stages * p.stage_bytes), lora_bu = lora_u + lora_b_offset(p);
+        const uint32_t lora_u = base_u + (kRing ? 0u : (uint32_t)(p.stages * p.stage_bytes)), lora_bu = lora_u + lora_b_offset(p);
         const uint64_t da0 = g_desc_k(base_u);
         const uint64_t db0 = MODE == kGFwd ? g_desc_k(base_u + (uint32_t)p.a_bytes) : g_desc_mn(base_u + (uint32_t)p.a_bytes, 8192);
         const uint64_t la0 = g_desc_k(lora_u);
@@ -441,16 +553,22 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4;
         for (Walk w(unit); rank == 0 && ok && w.next(p); ++acc) {
             const int m = w.tile % p.mt, buf = acc & 1;
-            const int first = w.lora_first(), spread = w.k1 - first;
             int blocks = LORA && waited ? p.list_len[m] : 0;
             if (acc >= 2 && !(ok = wait_warp(&tempty[buf], (uint32_t)(((acc >> 1) - 1) & 1), abort_flag, status, kGStMma,
                                              p.timeout_ns)))
                 break;
             const uint32_t d = tmem + (uint32_t)(buf * kGAccCols);
+            auto next_stage = [&]() {
+                __syncwarp();
+                if (++st == p.stages) {
+                    st = 0;
+                    ++use;
+                }
+            };
             // main stages [kb, stop) of the tile
             auto main_stages = [&](int kb, int stop) {
                 for (; kb < stop; ++kb) {
-                    if (!(ok = wait_warp(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
+                    if (!(ok = wait_warp(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns))) return false;
                     ptx::tc_fence_after();
                     if (leader) {
                         const uint64_t da = da0 + (uint32_t)st * stage16, db = db0 + (uint32_t)st * stage16;
@@ -459,57 +577,51 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             mma(d, da + ks * 2, db + ks * (MODE == kGFwd ? 2 : 128), id_main, kb > w.k0 || ks ? 1u : 0u);
                         commit(&empty[st]);
                     }
-                    __syncwarp();
-                    if (++st == p.stages) {
-                        st = 0;
-                        ++use;
-                    }
+                    next_stage();
                 }
+                return true;
             };
-            if (!LORA) {
-                main_stages(w.k0, w.k1);
-            } else {
-                // the tile's LoRA steps, evenly between the main stages from `first` on
-                int kb = first + 1;
-                main_stages(w.k0, kb);
-                if (ok && !waited) {
+            auto begin = [&](int& e, int& due) {
+                if (!waited) {
                     ptx::pdl_wait();
                     waited = true;
                     blocks = p.list_len[m];
                 }
                 blocks = __shfl_sync(0xffffffffu, blocks, 0);  // uniform, and so the walk
                 const int all = lora_steps(p, blocks);
-                int e = steps_begin(p, all, w.piece), due = steps_end(p, all, w.piece) - e;
-                const int ext = due;
-                while (ok) {
-                    for (; due >= spread; due -= spread, ++e) {
-                        if (!(ok = wait_warp(&lfull[lb], turn & 1, abort_flag, status, kGStMma, p.timeout_ns))) break;
-                        ptx::tc_fence_after();
-                        if (leader) {
-                            const uint32_t at = lb * ((uint32_t)p.lora_bytes >> 4);
-                            const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
-                            const int n = min(p.ups, blocks - (e >> 1) * p.ups);
-                            for (int h = 0; h < 2; ++h)
-                                for (int k = 0; k < n; ++k) {
-                                    const int c = h * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
-                                    mma(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
-                                                    lb0 + at + (uint32_t)(k * (MODE == kGFwd ? 128 : 2)), id_lora, 1u);
-                                }
-                            commit(&lempty[lb]);
+                e = steps_begin(p, all, w.piece);
+                due = steps_end(p, all, w.piece) - e;
+            };
+            auto step = [&](int e) {
+                if (!(ok = kRing ? wait_warp(&full[st], use & 1, abort_flag, status, kGStMma, p.timeout_ns)
+                                 : wait_warp(&lfull[lb], turn & 1, abort_flag, status, kGStMma, p.timeout_ns)))
+                    return false;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint32_t at = kRing ? (uint32_t)st * stage16 : lb * ((uint32_t)p.lora_bytes >> 4);
+                    const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
+                    const int n = min(p.ups, blocks - (e >> 1) * p.ups);
+                    for (int h = 0; h < 2; ++h)
+                        for (int k = 0; k < n; ++k) {
+                            const int c = h * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
+                            mma(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
+                                lb0 + at + (uint32_t)(k * (MODE == kGFwd ? 128 : 2)), id_lora, 1u);
                         }
-                        __syncwarp();
-                        if (++lb == (uint32_t)p.lbufs) {
-                            lb = 0;
-                            ++turn;
-                        }
-                    }
-                    if (!ok || kb >= w.k1) break;
-                    const int n = ext ? min((spread - due + ext - 1) / ext, w.k1 - kb) : w.k1 - kb;
-                    main_stages(kb, kb + n);
-                    kb += n;
-                    due += n * ext;
+                    commit(kRing ? &empty[st] : &lempty[lb]);
                 }
-            }
+                if (kRing) {
+                    next_stage();
+                } else {
+                    __syncwarp();
+                    if (++lb == (uint32_t)p.lbufs) {
+                        lb = 0;
+                        ++turn;
+                    }
+                }
+                return true;
+            };
+            if (LORA) walk_tile(w, MODE == kGFwd, main_stages, begin, step);
+            else main_stages(w.k0, w.k1);
             if (ok && leader) commit(&tfull[buf]);
             __syncwarp();
         }
@@ -521,23 +633,19 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         }
     } else if (warp >= kGBuilder0) {
         // ================================================================ LoRA steps
-        if (LORA) {
+        if (LORA && MODE == kGBwd) {
             ptx::pdl_wait();
             const int bt = threadIdx.x - kGBuilder0 * 32;
             // A builder's pieces lie in one column of 16-byte pieces, a fixed number of rows apart
             // (a multiple of eight, so their swizzle is the same): piece i of the operand in row
-            // a_row + i a_step, column a_c; of B in row b_row + i b_step, column b_c (forward a row is
-            // a rank, 16 to a block; backward an output column).
+            // a_row + i a_step, column a_c; of A_a in row b_row + i b_step (an output column), column b_c.
             const int a_lg = p.ups == 4 ? 4 : 3, a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
             const int a_rows = p.a_bytes >> 7;
             const int a_half = a_c >> (a_lg - 1), a_k = a_c & ((1 << (a_lg - 1)) - 1);  // hi or lo; piece of the blocks
-            const int b_lg = MODE == kGFwd ? (PAIR ? 3 : 4) : 2, b_c = bt & ((1 << b_lg) - 1), b_row = bt >> b_lg, b_step = kGBuilders >> b_lg;
+            const int b_c = bt & 3, b_row = bt >> 2, b_step = kGBuilders >> 2;
             const int b_cols = p.cols / kCtas, b_n0 = rank * b_cols;  // this CTA's columns of the tile
-            const int b_rows = MODE == kGFwd ? (b_c < b_cols >> 3 ? 16 * p.ups : 0) : b_cols;
             const uint32_t a_off = (uint32_t)((a_c >> 3) * p.a_bytes + a_row * 128 + (((a_c & 7) ^ (a_row & 7)) << 4));
-            const uint32_t b_off =
-                lora_b_offset(p) + (MODE == kGFwd ? (uint32_t)((b_c >> 3) * (p.ups * 2048) + b_row * 128 + (((b_c & 7) ^ (b_row & 7)) << 4))
-                                                  : (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4)));
+            const uint32_t b_off = lora_b_offset(p) + (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4));
             // the walk over the steps: step e of `ext` of the tile
             Walk w(unit);
             int e = -1, ext = 0, m = 0, n0 = 0, row0 = 0, blocks = 0;  // the tile's next step, where they end
@@ -555,23 +663,19 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < kGMaxA; ++i) {
                         const int row = a_row + i * a_step, tok = row0 + row;
-                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[MODE == kGFwd && p.order ? p.order[tok] : tok] : -2;
+                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
                     }
                 }
                 return true;
             };
-            // the blocks that the next step's pieces come from: one for the operand, one per pass of B
-            int ua, ub[kGMaxB];
+            // the blocks that the next step's pieces come from: of the operand, of A_a
+            int ua, ub;
             auto blocks_of_step = [&]() {
                 const int b0 = (e >> 1) * p.ups;
                 const int32_t* list = p.lists + (size_t)m * kListMax * kCtas;
-                const int ka = b0 + (a_k >> 1);
+                const int ka = b0 + (a_k >> 1), kb = b0 + (b_c >> 1);
                 ua = ka < blocks ? list[ka] : kNoBlock;
-#pragma unroll
-                for (int i = 0; i < kGMaxB; ++i) {
-                    const int kk = MODE == kGFwd ? (b_row + i * b_step) >> 4 : b_c >> 1, kb = b0 + kk;
-                    ub[i] = (MODE == kGFwd || i == 0) && kk < p.ups && kb < blocks ? list[kb] : kNoBlock;
-                }
+                ub = kb < blocks ? list[kb] : kNoBlock;
             };
             auto copy = [&](uint32_t buf) {  // the step's pieces into its buffer; zero where nothing belongs
                 const int s = e & 1;
@@ -585,19 +689,13 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                 }
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i) {
-                    const int row = b_row + i * b_step, u = MODE == kGFwd ? ub[i] : ub[0];
-                    if (row >= b_rows) continue;
-                    const uint16_t* pool = p.B + ((size_t)s * p.n_adapters + block_adapter(u)) * p.r_max * p.NC;
-                    if (MODE == kGFwd) {  // a row of B_a, eight columns
-                        const int j = row & 15;
-                        const bool in = j < block_live(u) && n0 + b_c * 8 < p.NC;
-                        ptx::cp_async16(buf + b_off + (uint32_t)(i * b_step * 128),
-                                        in ? pool + (size_t)(block_rank0(u) + j) * p.NC + n0 + b_c * 8 : p.B, in ? 16 : 0);
-                    } else {  // a row of A_a, eight ranks; what lies past the rank is not a number
-                        const int j = (b_c & 1) * 8, live = n0 + row < p.NC ? min(8, max(0, block_live(u) - j)) : 0;
-                        ptx::cp_async16(buf + b_off + (uint32_t)(i * b_step * 64),
-                                        live ? pool + (size_t)(n0 + row) * p.r_max + block_rank0(u) + j : p.B, 2 * live);
-                    }
+                    const int row = b_row + i * b_step;
+                    if (row >= b_cols) continue;
+                    const uint16_t* pool = p.B + ((size_t)s * p.n_adapters + block_adapter(ub)) * p.r_max * p.NC;
+                    // a row of A_a, eight ranks; what lies past the rank is not a number
+                    const int j = (b_c & 1) * 8, live = n0 + row < p.NC ? min(8, max(0, block_live(ub) - j)) : 0;
+                    ptx::cp_async16(buf + b_off + (uint32_t)(i * b_step * 64),
+                                    live ? pool + (size_t)(n0 + row) * p.r_max + block_rank0(ub) + j : p.B, 2 * live);
                 }
                 ptx::cp_async_commit();
             };
@@ -612,7 +710,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < kGMaxB; ++i)
                         if (odd >> i & 1) {
-                            uint4* v = reinterpret_cast<uint4*>(at + i * b_step * (MODE == kGFwd ? 128 : 64));
+                            uint4* v = reinterpret_cast<uint4*>(at + i * b_step * 64);
                             uint4 w = *v;
                             uint32_t* e = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
@@ -644,7 +742,7 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                 uint32_t marks = 0;
 #pragma unroll
                 for (int i = 0; i < kGMaxB; ++i)
-                    if (b_row + i * b_step < b_rows && block_bad(MODE == kGFwd ? ub[i] : ub[0])) marks |= 1u << i;
+                    if (b_row + i * b_step < b_cols && block_bad(ub)) marks |= 1u << i;
                 if (held == 0) odd = marks;
                 else odd_next = marks;
                 if (++lb == (uint32_t)p.lbufs) {
@@ -797,9 +895,9 @@ gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         if (rank == 0 && threadIdx.x < p.stages) {
             const int s = (int)threadIdx.x;
             const uint32_t mine = s_fills[s], other = ptx::ld_dsmem_u32(ptx::mapa(ptx::smem_u32(&s_fills[s]), 1));
-            const uint32_t half = (uint32_t)(p.a_bytes + p.b_bytes), fills = mine > other ? mine : other;
-            if (mine > other) ptx::mbar_complete_tx(&full[s], half);
-            if (mine < other) ptx::mbar_arrive_expect_tx(&full[s], half);
+            const uint32_t fills = mine > other ? mine : other;
+            if (mine > other) ptx::mbar_complete_tx(&full[s], s_tx[s]);
+            if (mine < other) ptx::mbar_arrive_expect_tx(&full[s], ptx::ld_dsmem_u32(ptx::mapa(ptx::smem_u32(&s_tx[s]), 1)));
             if (fills) wait_bar(&full[s], (fills - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns, false);
         }
         __syncwarp();
@@ -848,22 +946,24 @@ struct OperandParams {
         const float* v;  // `planes` planes of [2][M][r_max], summed in plane order
         int planes;
         uint16_t* ops;
-    } side[2];           // blockIdx.y; the lists are made with the first
+    } side[2];           // backward: blockIdx.y; the lists are made with the first
     long long plane;
     const int32_t* tok_adapter;
     const int32_t* order;  // as the GEMM's
+    const int32_t* indptr;
     const int32_t* ranks;
     const float* scales;
     int M, n_adapters, r_max, r16;
     const uint8_t* bad;  // [2][n_adapters][kGatedScanMax], bad_parts of them written (a multiple of 4)
     int bad_parts;
     int tile;  // tokens a list covers: 128 or 256
-    int32_t* lists;
-    int32_t* list_len;
+    int32_t *lists, *list_len, *list_base;
+    // forward: the GEMM's steps, see GatedSteps
+    int ups, rows, per_tile;
 };
 
 constexpr int kOpThreads = 256;
-constexpr int kOpRows = 16;  // tokens per CTA
+constexpr int kOpRows = 16;   // tokens per CTA
 constexpr int kPlanesMax = 8;
 
 // Whether the matrix of adapter a and slice s was marked as non-finite.
@@ -878,97 +978,201 @@ __device__ __forceinline__ bool marked(const OperandParams& p, int a, int s)
     return bad;
 }
 
-// s_a v of both slices as bf16 halves hi + lo (columns past the rank zero; NaN for an adapter whose
-// matrix is not finite, so that its own tokens show it: the GEMM's copy of the matrix has its
-// non-finite elements zeroed, and the other tokens' zeros stay zeros), and per token tile the rank blocks that its rows use, adapters in order of first appearance.
-// Lets the GEMM start at once (see the wait there).
+__device__ __forceinline__ int rank_of(const OperandParams& p, int a) { return max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max)); }
+
+// The rank blocks that a token tile's rows use, adapters in order of first appearance.
+struct TileBlocks {
+    alignas(16) int id[kOpThreads];  // per row: its adapter (-1: none),
+    int first[kOpThreads];           // the adapter's first block in the list,
+    int count[kOpThreads];           // and its blocks (0 without an adapter)
+    int warp[kOpThreads / 32];
+    int total;
+};
+// Nothing in it waits for the shrink: the kernels do it before their wait.
+__device__ __forceinline__ bool tile_blocks(const OperandParams& p, int m, TileBlocks& t)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = m * p.tile + tid;
+    int id = tid < p.tile && row < p.M ? p.tok_adapter[p.order ? p.order[row] : row] : -1;
+    if (id >= p.n_adapters) id = -1;
+    t.id[tid] = id;
+    __syncthreads();
+    int f = tid;  // the first row of the same adapter
+    for (int j = (tid & ~3) - 4; j >= 0; j -= 4) {
+        const int4 o = *reinterpret_cast<const int4*>(t.id + j);
+        f = o.x == id ? j : o.y == id ? j + 1 : o.z == id ? j + 2 : o.w == id ? j + 3 : f;
+    }
+    for (int j = tid - 1; j >= (tid & ~3); --j)
+        if (t.id[j] == id && j < f) f = j;
+    const int n = id >= 0 ? (rank_of(p, id) + 15) / 16 : 0;
+    const int mine = f == tid ? n : 0;
+    int at = mine;  // blocks up to this thread's, by a scan over the tile
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+    }
+    if (lane == 31) t.warp[warp] = at;
+    __syncthreads();
+    int total = 0;
+    at -= mine;
+    for (int w = 0; w < kOpThreads / 32; ++w) {
+        if (w < warp) at += t.warp[w];
+        total += t.warp[w];
+    }
+    t.first[tid] = at;
+    t.count[tid] = n;
+    if (tid == 0) t.total = total;
+    __syncthreads();
+    at = t.first[f];
+    __syncthreads();
+    t.first[tid] = at;
+    __syncthreads();
+    return mine > 0;
+}
+// The list, by the threads whose row is its adapter's first.
+__device__ __forceinline__ void write_list(const OperandParams& p, int m, const TileBlocks& t, bool first)
+{
+    if (first) {
+        const int id = t.id[threadIdx.x], at = t.first[threadIdx.x], n = t.count[threadIdx.x];
+        const int rank = rank_of(p, id);
+        int32_t* list = p.lists + (size_t)m * kListMax * (p.tile / kGTileM);
+        const int bad = (marked(p, id, 0) ? 1 : 0) | (marked(p, id, 1) ? 2 : 0);
+        for (int b = 0; b < n; ++b) list[at + b] = block_code(id, b, min(16, rank - 16 * b), bad);
+    }
+    if (threadIdx.x == 0) p.list_len[m] = t.total;
+}
+
+// Eight ranks of s_a v (columns past the rank zero; NaN for an adapter whose matrix is not finite, so
+// that its own tokens show it: the GEMM takes that matrix, or its non-finite elements, as zeros, and
+// the other tokens' zeros stay zeros), and their bf16 half hi (h == 0) or lo.
+struct Eight {
+    float f[8];
+    // planes of v; the rank and scale of the token's adapter
+    __device__ __forceinline__ void load(const OperandParams& p, const float* planes, int n_planes, int s, int tok, int r, float scale,
+                                         int c, bool bad)
+    {
+        float4 v[kPlanesMax][2];
+        const float* src = planes + ((size_t)s * p.M + tok) * p.r_max + 8 * c;
+#pragma unroll
+        for (int k = 0; k < kPlanesMax; ++k)
+            if (k < n_planes && 8 * c < p.r_max) {
+                v[k][0] = *reinterpret_cast<const float4*>(src + k * p.plane);
+                v[k][1] = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPlanesMax; ++k)
+            if (k < n_planes && 8 * c < r) {
+                f[0] += v[k][0].x; f[1] += v[k][0].y; f[2] += v[k][0].z; f[3] += v[k][0].w;
+                f[4] += v[k][1].x; f[5] += v[k][1].y; f[6] += v[k][1].z; f[7] += v[k][1].w;
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = bad ? __uint_as_float(0x7fc00000u) : 8 * c + e < r ? scale * f[e] : 0.f;
+    }
+    // the values' bf16 half; what it leaves stays
+    __device__ __forceinline__ uint4 half()
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            f[2 * e] -= bf16_lo(w[e]);
+            f[2 * e + 1] -= bf16_hi(w[e]);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Backward: s_a v of both slices as bf16 halves [2][M][hi r16 | lo r16], and the token tiles' lists. Lets
+// the GEMM start at once (see the wait there).
 __global__ void __launch_bounds__(kOpThreads)
 operand_kernel(const OperandParams p)
 {
+    __shared__ TileBlocks t;
     ptx::pdl_launch_dependents();
+    const int tid = threadIdx.x, per = p.tile / kOpRows, m = (int)blockIdx.x / per;
+    const bool lists = !blockIdx.y && (int)blockIdx.x % per == 0;  // one CTA of the tile makes its list
+    const bool first = lists && tile_blocks(p, m, t);
     ptx::pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto& d = p.side[blockIdx.y];
     const int chunks = p.r16 >> 3, items = 2 * kOpRows * chunks;
     for (int i = tid; i < items; i += kOpThreads) {
         const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
         const int row = (int)blockIdx.x * kOpRows + rs % kOpRows;
         if (row >= p.M) continue;
-        // everything that does not wait for the adapter first: the planes (past r_max: none; of a
-        // row without an adapter: whatever is there, not used)
-        const int tok = p.order ? p.order[row] : row, a = p.tok_adapter[tok];
-        float4 v[kPlanesMax][2];
-        const float* src = d.v + ((size_t)s * p.M + tok) * p.r_max + 8 * c;
-#pragma unroll
-        for (int k = 0; k < kPlanesMax; ++k)
-            if (k < d.planes && 8 * c < p.r_max) {
-                v[k][0] = *reinterpret_cast<const float4*>(src + k * p.plane);
-                v[k][1] = *reinterpret_cast<const float4*>(src + k * p.plane + 4);
-            }
+        const int a = p.tok_adapter[row];
         if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
-        const bool bad = blockIdx.y == 0 && marked(p, a, s);
-        const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
-        const float scale = p.scales ? p.scales[a] : 1.f;
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < kPlanesMax; ++k)
-            if (k < d.planes && 8 * c < r) {
-                f[0] += v[k][0].x; f[1] += v[k][0].y; f[2] += v[k][0].z; f[3] += v[k][0].w;
-                f[4] += v[k][1].x; f[5] += v[k][1].y; f[6] += v[k][1].z; f[7] += v[k][1].w;
-            }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 8 * c + e < r ? scale * f[e] : 0.f;
-        if (bad)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7fc00000u);
+        Eight v;
+        v.load(p, d.v, d.planes, s, row, rank_of(p, a), p.scales ? p.scales[a] : 1.f, c, blockIdx.y == 0 && marked(p, a, s));
         uint4* o = reinterpret_cast<uint4*>(d.ops + ((size_t)s * p.M + row) * (2 * p.r16));
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-                f[2 * e] -= bf16_lo(w[e]);
-                f[2 * e + 1] -= bf16_hi(w[e]);
-            }
-            o[part * chunks + c] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[c] = v.half();
+        o[chunks + c] = v.half();
+    }
+    if (lists) write_list(p, m, t, first);
+}
+
+// Forward: the operand as the GEMM's steps have it, zeros in the blocks of other adapters written out,
+// so that a step is a few boxes of the GEMM's ring: step e (slice e & 1) of a tile is ups / 2
+// arrays [rows][64] of bf16, four groups of 16 columns each (ups of hi, ups of lo), from array
+// (2 base + e) ups / 2 on. The bases grow by what the tiles before can need at most: tokens that
+// come by adapter have (adapters before the tile's first + tiles before it) R blocks at most, R =
+// ceil(r_max / 16); in the caller's order every tile may need per_tile steps.
+__global__ void __launch_bounds__(kOpThreads)
+expand_kernel(const OperandParams p)
+{
+    ptx::pdl_launch_dependents();
+    __shared__ TileBlocks t;
+    __shared__ int s_base;
+    const int tid = threadIdx.x, per = p.tile / kOpRows, m = (int)blockIdx.x / per, row0 = (int)blockIdx.x % per * kOpRows;
+    if (m * p.tile + row0 >= p.M) return;
+    const bool first = tile_blocks(p, m, t);
+    if (p.per_tile < 0) {
+        int before = 0;  // adapters with tokens before the tile's first
+        for (int a0 = 0; a0 < t.id[0]; a0 += kOpThreads) {
+            const int a = a0 + tid;
+            before += __syncthreads_count(a < t.id[0] && p.indptr[a + 1] > p.indptr[a]);
         }
+        if (tid == 0) s_base = ((before + m) * (p.r16 >> 4) + (p.ups - 1) * m) / p.ups;
+    } else if (tid == 0) {
+        s_base = m * p.per_tile;
     }
-    const int per = p.tile / kOpRows, m = (int)blockIdx.x / per;
-    if (blockIdx.y || (int)blockIdx.x % per) return;  // one CTA of the tile makes its list
-    __shared__ __align__(16) int s_id[kOpThreads];
-    __shared__ int s_cnt[kOpThreads / 32];
-    const int row = m * p.tile + tid;
-    int id = tid < p.tile && row < p.M ? p.tok_adapter[p.order ? p.order[row] : row] : -1;
-    if (id >= p.n_adapters) id = -1;
-    s_id[tid] = id;
     __syncthreads();
-    bool first = id >= 0;
-    for (int j = 0; j < (tid & ~3); j += 4) {
-        const int4 o = *reinterpret_cast<const int4*>(s_id + j);
-        first = first && o.x != id && o.y != id && o.z != id && o.w != id;
+    const auto& d = p.side[0];
+    const int base = s_base, steps = 2 * ((t.total + p.ups - 1) / p.ups), lg = p.ups == 4 ? 4 : 3;
+    // where a 16-byte piece of a step's row is: groups of 16 columns, four to an array
+    auto piece_at = [&](int e, int piece, int row) {
+        return reinterpret_cast<uint4*>(d.ops) + (((size_t)(2 * base + e) * (p.ups >> 1) + (piece >> 3)) * p.rows + row) * 8 + (piece & 7);
+    };
+    for (int i = tid; i < steps * kOpRows << lg; i += kOpThreads) {
+        const int piece = i & ((1 << lg) - 1), row = row0 + ((i >> lg) & (kOpRows - 1)), e = (i >> lg) / kOpRows;
+        const int b = (e >> 1) * p.ups + ((piece >> 1) & (p.ups - 1)) - t.first[row];
+        if (m * p.tile + row < p.M && (b < 0 || b >= t.count[row])) *piece_at(e, piece, row) = make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int j = tid & ~3; j < tid; ++j) first = first && s_id[j] != id;
-    // rank blocks before this thread's, by a scan over the tile
-    const int rank = first ? max(1, min(p.ranks ? p.ranks[id] : p.r_max, p.r_max)) : 0, mine = (rank + 15) / 16;
-    int at = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += v;
+    // this thread's eight ranks of a row and slice
+    static_assert(2 * kOpRows * (LORA_MAX_RANK / 8) <= kOpThreads, "a thread has one piece");
+    const int chunks = p.r16 >> 3, c = tid % chunks, mine = tid / chunks, s = mine & 1, row = row0 + (mine >> 1), pos = m * p.tile + row;
+    const bool live = mine < 2 * kOpRows && pos < p.M && (c >> 1) < t.count[row];
+    int a = 0, tok = 0, r = 0;
+    float scale = 1.f;
+    if (live) {
+        a = t.id[row];
+        tok = p.order ? p.order[pos] : pos;
+        r = rank_of(p, a);
+        if (p.scales) scale = p.scales[a];
     }
-    if (lane == 31) s_cnt[warp] = at;
-    __syncthreads();
-    int total = 0;
-    at -= mine;
-    for (int w = 0; w < kOpThreads / 32; ++w) {
-        if (w < warp) at += s_cnt[w];
-        total += s_cnt[w];
+    ptx::pdl_wait();  // from here on what the shrink wrote
+    if (live) {
+        Eight v;
+        v.load(p, d.v, d.planes, s, tok, r, scale, c, marked(p, a, s));
+        const int b = t.first[row] + (c >> 1), e = 2 * (b / p.ups) + s, piece = (b % p.ups) * 2 + (c & 1);
+        *piece_at(e, piece, row) = v.half();
+        *piece_at(e, 2 * p.ups + piece, row) = v.half();
     }
-    int32_t* list = p.lists + (size_t)m * kListMax * (p.tile / kGTileM);
-    const bool bad = first && (marked(p, id, 0) || marked(p, id, 1));
-    for (int b = 0; b < mine; ++b) list[at + b] = block_code(id, b, min(16, rank - 16 * b), bad);
-    if (tid == 0) p.list_len[m] = total;
+    if (row0 == 0) {
+        write_list(p, m, t, first);
+        if (tid == 0) p.list_base[m] = base;
+    }
 }
 
 // LoRA step buffers beside a ring of enough stages (36 tokens of 32 adapters: one 56 us, two or three 48).
@@ -980,14 +1184,14 @@ int lora_buffers(const GatedParams& p, int room, bool pair)
 }
 
 template <int MODE, bool LORA, bool PAIR>
-cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int grid, cudaStream_t stream)
+cudaError_t launch_mode(const GatedMaps& maps, const GatedParams& p, int grid, cudaStream_t stream)
 {
     auto kern = gated_gemm_kernel<MODE, LORA, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kGThreads, 1, 1);
+    cfg.blockDim = dim3(MODE == kGFwd ? kGFwdThreads : kGThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -999,7 +1203,7 @@ cudaError_t launch_mode(const CUtensorMap (&tm)[4], const GatedParams& p, int gr
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+    return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 // Pairs of CTAs that the current device runs at once (an SM without a partner stays idle).
@@ -1013,7 +1217,7 @@ int pair_count()
     auto kern = gated_gemm_kernel<kGFwd, true, true>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2), 1, 1);
-    cfg.blockDim = dim3(kGThreads, 1, 1);
+    cfg.blockDim = dim3(kGFwdThreads, 1, 1);
     cfg.dynamicSmemBytes = kGSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1123,7 +1327,53 @@ size_t gated_operand_bytes(int M, int r_max)
 }
 size_t gated_list_bytes(int M)
 {
-    return (size_t)(M + 2 * kGTileM - 1) / (2 * kGTileM) * 2 * (kListMax + 1) * 4;
+    return (size_t)(M + 2 * kGTileM - 1) / (2 * kGTileM) * 2 * (kListMax + 2) * 4;
+}
+
+namespace {
+
+// Steps per slice that expand_kernel's bases may reach, for tiles of `tile` tokens.
+size_t gated_steps(int M, int tile, int ups, bool order, int n_adapters, int r_max)
+{
+    const size_t mt = (size_t)(M + tile - 1) / tile, R = (size_t)(r_max + 15) / 16;
+    const size_t all = n_adapters < M ? n_adapters : M, in_tile = all < (size_t)tile ? all : (size_t)tile;
+    if (!order) return mt * ((in_tile * R + ups - 1) / ups);
+    return ((all + mt) * R + (ups - 1) * mt) / ups + 1;
+}
+// Rows of a step's arrays, and their bytes in the ring.
+int gated_a_rows(int M) { return M >= kGTileM ? kGTileM : (M + 7) / 8 * 8; }
+// The forward's rank blocks per step and its ring's stage, where a step has to fit: four with few tokens
+// (whose operand is short) or where that much is free in a stage, else two.
+struct FwdSteps {
+    int ups, stage;
+};
+FwdSteps gated_fwd_steps(const GatedPlan& plan, int M)
+{
+    const int ctas = plan.pair ? 2 : 1, a = gated_a_rows(M) * 128, stage = a + 2 * plan.cols * 128 / ctas;
+    const int four = 2 * a + (plan.cols / ctas + 63) / 64 * 4 * 2048;
+    if (four <= stage) return {4, stage};
+    if (a <= kGTileM / 2 * 128) return {4, four};
+    return {2, stage};
+}
+
+}  // namespace
+
+// The largest of what the plans for M tokens need. A batch of several tiles keeps the caller's order only where
+// its pool has few rank blocks (gated_order: fewer than 2 (6 + R)).
+size_t gated_expand_bytes(int M, int n_adapters, int r_max)
+{
+    const size_t R = (size_t)(r_max + 15) / 16;
+    size_t most = 0;
+    for (int tile = kGTileM; tile <= 2 * kGTileM; tile += kGTileM) {
+        const size_t rows = M > kGTileM ? tile : gated_a_rows(M);
+        const int few = (int)((2 * (6 + R)) / R + 1), kept = M > tile && n_adapters > few ? few : n_adapters;
+        for (int ups = 2; ups <= 4; ups += 2) {
+            const size_t a = gated_steps(M, tile, ups, false, kept, r_max), b = gated_steps(M, tile, ups, true, n_adapters, r_max);
+            const size_t bytes = (a > b ? a : b) * 2 * (ups / 2) * rows * 128;
+            if (bytes > most) most = bytes;
+        }
+    }
+    return most;
 }
 
 size_t gated_gather_bytes(int M, int K) { return M > kGTileM ? (size_t)M * K * 2 : 0; }
@@ -1160,7 +1410,9 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     p.bad = bad;
     p.bad_parts = gated_scan_parts(sides[0].down, M, pool);
     p.tok_adapter = seg.tok_adapter;
-    if (gated_order(plan, backward, M, pool.n_adapters, pool.r_max)) p.order = seg.perm;
+    const bool order = gated_order(plan, backward, M, pool.n_adapters, pool.r_max);
+    if (order) p.order = seg.perm;
+    p.indptr = seg.indptr;
     p.ranks = pool.ranks;
     p.scales = pool.scales;
     p.M = M;
@@ -1169,6 +1421,12 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     p.r16 = (pool.r_max + 15) / 16 * 16;
     p.lists = static_cast<int32_t*>(lists);
     p.list_len = p.lists + (size_t)plan.mt * kListMax * (p.tile / kGTileM);
+    p.list_base = p.list_len + plan.mt;
+    if (!backward) {
+        p.ups = gated_fwd_steps(plan, M).ups;
+        p.rows = plan.pair ? 2 * kGTileM : gated_a_rows(M);
+        p.per_tile = order ? -1 : (int)(gated_steps(M, p.tile, p.ups, false, pool.n_adapters, pool.r_max) / plan.mt);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.mt * (p.tile / kOpRows)), (unsigned)n, 1);
     cfg.blockDim = dim3(kOpThreads, 1, 1);
@@ -1178,7 +1436,7 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, operand_kernel, p);
+    return backward ? cudaLaunchKernelEx(&cfg, operand_kernel, p) : cudaLaunchKernelEx(&cfg, expand_kernel, p);
 }
 
 cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
@@ -1205,7 +1463,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     p.kb = bwd ? 2 * p.kb_half : p.kb_half;
     // few tokens: only their rows (in eights) are loaded; the MMA's other rows read whatever
     // the shared memory holds and land in accumulator rows that nobody drains
-    const int a_rows = a.M >= kGTileM ? kGTileM : (a.M + 7) / 8 * 8;
+    const int a_rows = gated_a_rows(a.M);
     p.a_bytes = a_rows * 128;
     p.b_bytes = p.bn * 128 / (plan.pair ? 2 : 1);
     p.stage_bytes = p.a_bytes + p.b_bytes;
@@ -1214,12 +1472,14 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     // shrink). At the end: what the MMA may read past a short operand tile.
     p.smem = a_rows > kGTileM / 2 ? kGSmem : kGSmemShort;
     int room = p.smem - (kGTileM - a_rows) * 128 - kGBarBytes - 1024;
-    if (a.lora) {
+    if (a.lora && !bwd) {
+        const FwdSteps f = gated_fwd_steps(plan, a.M);
+        p.ups = f.ups;
+        p.stage_bytes = f.stage;
+    } else if (a.lora) {
         p.r16 = (a.r_max + 15) / 16 * 16;
-        // rank blocks per step: what four pieces per builder and the space beside four stages hold
-        p.ups = !bwd && a_rows <= 64 ? 4 : 2;
-        const int half = p.cols / (plan.pair ? 2 : 1);
-        p.lora_bytes = (int)lora_b_offset(p) + (bwd ? half * 64 : (half + 63) / 64 * p.ups * 2048);
+        p.ups = 2;  // what four pieces per builder and the space beside four stages hold
+        p.lora_bytes = (int)lora_b_offset(p) + p.cols / (plan.pair ? 2 : 1) * 64;
         p.lora_bytes = (p.lora_bytes + 1023) / 1024 * 1024;
         p.lbufs = lora_buffers(p, room, plan.pair);
         room -= p.lbufs * p.lora_bytes;
@@ -1242,29 +1502,41 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.B = static_cast<const uint16_t*>(a.B);
         p.lists = static_cast<const int32_t*>(a.lists);
         p.list_len = p.lists + (size_t)p.mt * kListMax * (plan.pair ? 2 : 1);
+        p.list_base = p.list_len + p.mt;
         p.tok_adapter = a.tok_adapter;
         if (gated_order(plan, bwd, a.M, a.n_adapters, a.r_max)) p.order = a.order;
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
     }
-    CUtensorMap tm[4];
+    GatedMaps maps;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     bool ok = true;
     for (int i = 0; i < 2; ++i) {
-        ok = ok && encode_tmap_2d(&tm[i], dt, bwd || p.order ? a.a[i] : a.a[0], (uint64_t)red, (uint64_t)a.M, (uint64_t)red * 2,
+        ok = ok && encode_tmap_2d(&maps.a[i], dt, bwd || p.order ? a.a[i] : a.a[0], (uint64_t)red, (uint64_t)a.M, (uint64_t)red * 2,
                                   kGKBlock, (uint32_t)a_rows, sw);
-        ok = ok && encode_tmap_2d(&tm[2 + i], dt, a.W[i], (uint64_t)a.K, (uint64_t)a.F, (uint64_t)a.K * 2, kGKBlock,
+        ok = ok && encode_tmap_2d(&maps.b[i], dt, a.W[i], (uint64_t)a.K, (uint64_t)a.F, (uint64_t)a.K * 2, kGKBlock,
                                   bwd ? kGKBlock : (uint32_t)p.cols, sw);
+    }
+    if (a.lora && !bwd) {
+        const size_t rows = plan.pair ? 2 * kGTileM : a_rows;
+        const size_t steps = gated_steps(a.M, plan.pair ? 2 * kGTileM : kGTileM, p.ups, p.order != nullptr, a.n_adapters, a.r_max);
+        ok = ok && encode_tmap_2d(&maps.e, dt, a.ops, 64, steps * 2 * (p.ups / 2) * rows, 128, 64, (uint32_t)a_rows, sw);
+        const uint64_t dims[3] = {(uint64_t)a.F, (uint64_t)a.r_max, (uint64_t)(2 * a.n_adapters)};
+        const uint64_t strides[2] = {(uint64_t)a.F * 2, (uint64_t)a.F * a.r_max * 2};
+        for (int b = 0; b < kRankBoxes; ++b) {
+            const uint32_t box[3] = {64, 1u << b, 1};
+            ok = ok && encode_tmap_3d(&maps.l[b], dt, a.B, dims, strides, box, sw);
+        }
     }
     if (!ok) return cudaErrorInvalidValue;
     const int grid = p.units * (plan.pair ? 2 : 1);
     if (plan.pair) {
-        if (bwd) return a.lora ? launch_mode<kGBwd, true, true>(tm, p, grid, stream) : launch_mode<kGBwd, false, true>(tm, p, grid, stream);
-        return a.lora ? launch_mode<kGFwd, true, true>(tm, p, grid, stream) : launch_mode<kGFwd, false, true>(tm, p, grid, stream);
+        if (bwd) return a.lora ? launch_mode<kGBwd, true, true>(maps, p, grid, stream) : launch_mode<kGBwd, false, true>(maps, p, grid, stream);
+        return a.lora ? launch_mode<kGFwd, true, true>(maps, p, grid, stream) : launch_mode<kGFwd, false, true>(maps, p, grid, stream);
     }
-    if (bwd) return a.lora ? launch_mode<kGBwd, true, false>(tm, p, grid, stream) : launch_mode<kGBwd, false, false>(tm, p, grid, stream);
-    return a.lora ? launch_mode<kGFwd, true, false>(tm, p, grid, stream) : launch_mode<kGFwd, false, false>(tm, p, grid, stream);
+    if (bwd) return a.lora ? launch_mode<kGBwd, true, false>(maps, p, grid, stream) : launch_mode<kGBwd, false, false>(maps, p, grid, stream);
+    return a.lora ? launch_mode<kGFwd, true, false>(maps, p, grid, stream) : launch_mode<kGFwd, false, false>(maps, p, grid, stream);
 }
 
 }  // namespace lora

@@ -99,6 +99,7 @@ size_t gated_gather_bytes(int M, int K);
 cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
                                 cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
+size_t gated_expand_bytes(int M, int n_adapters, int r_max);
 size_t gated_list_bytes(int M);
 size_t gated_part_bytes();
 size_t gated_count_bytes();
