@@ -72,7 +72,8 @@ constexpr int kGProducer = kGDrainWarps, kGMma = kGProducer + 1, kGBuilder0 = kG
 constexpr int kGBuilders = 256;
 constexpr int kGMaxA = 4, kGMaxB = 4;        // 16-byte pieces of a LoRA step per builder
 constexpr int kGThreads = (kGBuilder0 + kGBuilders / 32) * 32;
-constexpr int kGFwdThreads = kGBuilder0 * 32;  // the forward has no builders
+constexpr int kGLoaders = 4;                   // the forward's warps behind the issuer: B of a step, a block each
+constexpr int kGFwdThreads = (kGBuilder0 + kGLoaders) * 32;
 constexpr int kGTileM = 128;
 constexpr int kGMaxStages = 12;
 constexpr int kGKBlock = 64;                  // K per stage: 128 bytes of bf16, one swizzle row
@@ -321,6 +322,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
     __shared__ int s_last;       // this CTA's part of a shared tile was the last
     __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader,
     __shared__ uint32_t s_tx[kGMaxStages];     // and the bytes of each one's last fill
+    __shared__ int4 s_job[2];                  // a step for the loaders: stage (-1: the end), tile, first block, slice
     constexpr int kCtas = PAIR ? 2 : 1, kTokens = kCtas * kGTileM;
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int unit = (int)blockIdx.x / kCtas;
@@ -392,10 +394,6 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
             if (PAIR) ptx::tma_load_2d_pair(dst, map, leaders(&full[st]), c0, c1);
             else ptx::tma_load_2d(dst, map, &full[st], c0, c1);
         };
-        auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
-            if (PAIR) ptx::tma_load_3d_pair(dst, map, leaders(&full[st]), c0, c1, c2);
-            else ptx::tma_load_3d(dst, map, &full[st], c0, c1, c2);
-        };
         auto stage_free = [&]() {
             return ok = use == 0 || wait_warp(&empty[st], (use - 1) & 1, abort_flag, status, kGStRing, p.timeout_ns);
         };
@@ -414,14 +412,21 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
         // where a tile's rows of x are (see RowRun), of the next tile's a tile ahead
         RowRun run, next_run;
         if (kRing && p.order && unit < p.tiles) next_run.load(p.order, p.M, (unit % p.mt) * kTokens + rank * kGTileM, lane);
-        // the tile's rank blocks, lane l the l-th of 32; the next tile's a tile ahead
-        int blocks = 0, base = 0, codes = 0, next_blocks = 0, next_base = 0, next_codes = 0;
+        // the tile's rank blocks and where its steps' operands are; the next tile's a tile ahead
+        int blocks = 0, base = 0, next_blocks = 0, next_base = 0;
         auto fetch_list = [&](int tile) {
             if (tile >= p.tiles) return;
-            const int m = tile % p.mt;
-            next_blocks = p.list_len[m];
-            next_base = p.list_base[m];
-            next_codes = p.lists[(size_t)m * kListMax * kCtas + lane];
+            next_blocks = p.list_len[tile % p.mt];
+            next_base = p.list_base[tile % p.mt];
+        };
+        const uint64_t once = ptx::l2_policy_evict_first();
+        // A job for the loaders; they are done with the one before when they come to the barrier.
+        int jobs = 0;
+        auto hand_out = [&](int4 job) {
+            if (lane == 0) s_job[jobs & 1] = job;
+            ++jobs;
+            __syncwarp();
+            ptx::named_sync(1, (1 + kGLoaders) * 32);
         };
         bool waited = false;
         for (Walk w(unit); ok && w.next(p);) {
@@ -447,8 +452,13 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                             if (PAIR) {
                                 load(sb, &maps.b[rank], kb * kGKBlock, n0);
                             } else {
-                                load(sb, &maps.b[0], kb * kGKBlock, n0);
-                                load(sb + (uint32_t)(p.cols * 128), &maps.b[1], kb * kGKBlock, n0);
+                                // one token tile reads the weights once: they leave L2 to the adapters
+                                // (16 tokens, 8192 x 28672, 16 adapters: 158 us, without 163)
+                                for (int i = 0; i < 2; ++i)
+                                    if (kRing && p.mt == 1)
+                                        ptx::tma_load_2d_hint(sb + (uint32_t)(i * p.cols * 128), &maps.b[i], &full[st], kb * kGKBlock, n0, once);
+                                    else
+                                        load(sb + (uint32_t)(i * p.cols * 128), &maps.b[i], kb * kGKBlock, n0);
                             }
                         } else {
                             const bool up = kb >= p.kb_half;
@@ -474,49 +484,25 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                 }
                 blocks = __shfl_sync(0xffffffffu, next_blocks, 0);
                 base = __shfl_sync(0xffffffffu, next_base, 0);
-                codes = next_codes;
                 fetch_list(w.tile + p.units);
                 e = 0;
                 due = lora_steps(p, blocks);
             };
-            const int half = p.cols / kCtas;
-            const int rows = PAIR ? kTokens : p.a_bytes >> 7;
-            // this lane's part of a step's B: 64 columns of block k (of four)
-            const int k = lane & 3, atom = lane >> 2, x = n0 + rank * half + atom * 64, atoms = (half + 63) >> 6;
-            const uint32_t b_at = lora_b_offset(p) + (uint32_t)((atom * p.ups + k) * 2048);
-            const int32_t* list = p.lists + (size_t)(w.tile % p.mt) * kListMax * kCtas + lane;
-            auto step = [&](int e) {
-                const int s = e & 1, q = (e >> 1) * p.ups, n = min(p.ups, blocks - q);
+            const int atoms = (p.cols / kCtas + 63) >> 6, rows = PAIR ? kTokens : p.a_bytes >> 7;
+            auto step = [&](int e) {  // the operand; the loaders fetch B into the same stage
                 if (!stage_free()) return false;
-                if (s == 0 && q && (q & 31) == 0) codes = list[q];
+                hand_out(make_int4(st, w.tile, (e >> 1) * p.ups, e & 1));
                 const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes);
-                expect(lora_b_offset(p) + (uint32_t)(n * atoms * 2048));
+                expect(lora_b_offset(p) + (uint32_t)(min(p.ups, blocks - (e >> 1) * p.ups) * atoms * 2048));
                 if (leader)
                     for (int c = 0; c < p.ups / 2; ++c)
                         load(sa + (uint32_t)(c * p.a_bytes), &maps.e, 0, ((2 * base + e) * (p.ups / 2) + c) * rows + rank * kGTileM);
-                const int u = __shfl_sync(0xffffffffu, codes, (q + k) & 31);
-                if (k < n && atom < atoms) {
-                    // the block's live rows, then zeros (past the last matrix; a marked one is zeros too,
-                    // see Eight), in boxes of powers of two
-                    const int nothing = 2 * p.n_adapters, live = block_live(u);
-                    int z = block_bad(u) >> s & 1 ? nothing : s * p.n_adapters + block_adapter(u);
-                    for (int row = 0, left = live;;) {
-                        while (left) {
-                            const int b = 31 - __clz(left);
-                            load3(sa + b_at + (uint32_t)(row * 128), &maps.l[b], x, block_rank0(u) + row, z);
-                            row += 1 << b;
-                            left -= 1 << b;
-                        }
-                        if (row == 16) break;
-                        left = 16 - row;
-                        z = nothing;
-                    }
-                }
                 next_stage();
                 return true;
             };
             walk_tile(w, MODE == kGFwd, main_stages, begin, step);
         }
+        if (kRing) hand_out(make_int4(-1, 0, 0, 0));
         if (PAIR) {  // landed below, once both producers have stopped
             if (lane < p.stages) s_fills[lane] = use + (lane < st ? 1 : 0);
         } else {
@@ -630,6 +616,49 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
             if (leader) commit(mdone);
             __syncwarp();
             wait_warp(mdone, 0, abort_flag, status, kGStMma, p.timeout_ns, false);
+        }
+    } else if (kRing && warp >= kGBuilder0) {
+        // ================================================================ B of the LoRA steps
+        // A warp per block of a step, since issuing copies of changing shapes is what takes time (by the
+        // producer's lanes alone a step took 1 us, which was all that 64 tokens of 64 adapters of rank
+        // 64 waited for: 169 us, 148 with the loaders).
+        const int k = warp - kGBuilder0, atoms = (p.cols / kCtas + 63) >> 6;
+        int m = -1, q = 0, u = 0, ahead = 0;  // this warp's block of the last step, of the one after it
+        for (int jobs = 0;; ++jobs) {
+            ptx::named_sync(1, (1 + kGLoaders) * 32);
+            const int4 job = s_job[jobs & 1];
+            if (job.x < 0) break;
+            if (jobs == 0) ptx::pdl_wait();
+            if (k >= p.ups) continue;
+            const int jm = job.y % p.mt, s = job.w;
+            if (jm != m || job.z != q) {
+                const int32_t* list = p.lists + (size_t)jm * kListMax * kCtas + job.z + k;
+                const int left = p.list_len[jm] - job.z - k;  // blocks from this one on
+                u = left <= 0 ? kNoBlock : jm == m && job.z == q + p.ups ? ahead : list[0];
+                ahead = left > p.ups ? list[p.ups] : kNoBlock;
+                m = jm;
+                q = job.z;
+            }
+            if (u != kNoBlock && lane < atoms) {
+                // the block's live rows, then zeros (past the last matrix; a marked one is zeros too, see
+                // Eight), in boxes of powers of two
+                const int x = (job.y / p.mt) * p.cols + rank * (p.cols / kCtas) + lane * 64, nothing = 2 * p.n_adapters;
+                const uint32_t dst = base_u + (uint32_t)(job.x * p.stage_bytes) + lora_b_offset(p) + (uint32_t)((lane * p.ups + k) * 2048);
+                int z = block_bad(u) >> s & 1 ? nothing : s * p.n_adapters + block_adapter(u);
+                for (int row = 0, left = block_live(u);;) {
+                    while (left) {
+                        const int b = 31 - __clz(left), y = block_rank0(u) + row;
+                        if (PAIR) ptx::tma_load_3d_pair(dst + (uint32_t)(row * 128), &maps.l[b], leaders(&full[job.x]), x, y, z);
+                        else ptx::tma_load_3d(dst + (uint32_t)(row * 128), &maps.l[b], &full[job.x], x, y, z);
+                        row += 1 << b;
+                        left -= 1 << b;
+                    }
+                    if (row == 16) break;
+                    left = 16 - row;
+                    z = nothing;
+                }
+            }
+            __syncwarp();
         }
     } else if (warp >= kGBuilder0) {
         // ================================================================ LoRA steps
