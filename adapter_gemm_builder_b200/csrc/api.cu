@@ -665,7 +665,7 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
     if (pool) {
-        const GatedSide side = {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops};
+        const GatedSide side = {true, x, 0, false, reinterpret_cast<float*>(w + l.v), w + l.ops};
         if (launch_gated_gather(x, M, *pool, *seg, g8 != nullptr, w + l.rows, s) != cudaSuccess) return LORA_ERR_CUDA;
         if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
         a.lora = true;
@@ -705,7 +705,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     uint16_t* du = dg + (size_t)M * F;
     // 1. dg, du (and h) from the checkpoints
     int* count = reinterpret_cast<int*>(w + l.count);
-    if (launch_gated_point(dh, M, F, act, *g8, *u8, dg, du, h, count, s) != cudaSuccess) return LORA_ERR_CUDA;
+    const bool by_adapter = pool && gated_by_adapter(true, M, *pool, false);
+    if (launch_gated_point(dh, M, F, act, *g8, *u8, by_adapter ? seg->perm : nullptr, dg, du, h, count, s) != cudaSuccess) return LORA_ERR_CUDA;
     GatedGemmArgs a = {};
     a.backward = true;
     a.M = M;
@@ -725,8 +726,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
         if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
         x = w + l.x;
     }
-    const GatedSide sides[2] = {{false, dg, (int64_t)M * F, reinterpret_cast<float*>(w + l.u), w + l.ops_u},
-                                {true, x, 0, reinterpret_cast<float*>(w + l.v), w + l.ops_v}};
+    const GatedSide sides[2] = {{false, dg, (int64_t)M * F, by_adapter, reinterpret_cast<float*>(w + l.u), w + l.ops_u},
+                                {true, x, 0, false, reinterpret_cast<float*>(w + l.v), w + l.ops_v}};
     if (gated_operands(sides, 2, true, false, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
@@ -734,11 +735,12 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.lists = w + l.lists;
     a.B = pool->A;
     a.tok_adapter = seg->tok_adapter;
+    a.order = seg->perm;
     a.n_adapters = pool->n_adapters;
     a.r_max = pool->r_max;
     if (launch_gated_gemm(a, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 4. the adapters' gradients
-    return cuda_status(launch_gated_outer(x, w + l.ops_u, dA, dg, w + l.ops_v, dB, M, *pool, *seg, s));
+    return cuda_status(launch_gated_outer(x, w + l.ops_u, dA, dg, w + l.ops_v, dB, M, *pool, *seg, by_adapter, s));
 }
 
 int lora_switch_merge(const void* W, int N, int K, const lora_pool_t* pool, const int32_t* sel,

@@ -28,8 +28,7 @@
 // and the checkpoints are written to the tokens' own rows. (2048 tokens mixed over 48 adapters of
 // rank 16: 940 us in their own order, 298 in this; over 16 of rank 64 1480, 336. TMA's gather of four
 // rows at a time took 1.2 us a stage instead of .4.)
-// The backward keeps the caller's order: its sums are long beside its steps (mixed 463 us,
-// sorted 407; 672 and 551).
+// The backward writes dg and du in that order to begin with (gated_order says when).
 //
 // More than 128 tokens usually run on pairs of CTAs (cta_group::2, clusters of two): 256 tokens by
 // the same columns, each CTA with its 128 rows of A and half of B (forward: the even CTA the
@@ -692,7 +691,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
 #pragma unroll
                     for (int i = 0; i < kGMaxA; ++i) {
                         const int row = a_row + i * a_step, tok = row0 + row;
-                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[tok] : -2;
+                        ids[i] = row < a_rows && tok < p.M ? p.tok_adapter[p.order ? p.order[tok] : tok] : -2;
                     }
                 }
                 return true;
@@ -798,7 +797,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
             const int row0 = (w.tile % p.mt) * kTokens + rank * kGTileM + q * 32, n0 = (w.tile / p.mt) * p.cols, buf = acc & 1;
             const int row = row0 + lane;
             // the row's place in the outputs
-            const int out_row = MODE == kGFwd && LORA && p.order && row < p.M ? p.order[row] : row;
+            const int out_row = LORA && p.order && row < p.M ? p.order[row] : row;
             if (!wait_role(3, kGDrainWarps * 32, threadIdx.x == 0, &tfull[buf], (uint32_t)((acc >> 1) & 1), abort_flag, status,
                            kGStDrain, p.timeout_ns))
                 break;
@@ -1130,10 +1129,10 @@ operand_kernel(const OperandParams p)
         const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
         const int row = (int)blockIdx.x * kOpRows + rs % kOpRows;
         if (row >= p.M) continue;
-        const int a = p.tok_adapter[row];
+        const int tok = p.order ? p.order[row] : row, a = p.tok_adapter[tok];
         if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
         Eight v;
-        v.load(p, d.v, d.planes, s, row, rank_of(p, a), p.scales ? p.scales[a] : 1.f, c, blockIdx.y == 0 && marked(p, a, s));
+        v.load(p, d.v, d.planes, s, tok, rank_of(p, a), p.scales ? p.scales[a] : 1.f, c, blockIdx.y == 0 && marked(p, a, s));
         uint4* o = reinterpret_cast<uint4*>(d.ops + ((size_t)s * p.M + row) * (2 * p.r16));
         o[c] = v.half();
         o[chunks + c] = v.half();
@@ -1268,14 +1267,17 @@ struct GatedPlan {
     int split;  // pieces of the last round's tiles, 1: they stay whole
 };
 
-// Whether the GEMM takes its tokens by adapter: where it saves a unit six rank blocks or more, if the
-// batch is mixed. (The launch costs a sorted batch 1 us and the copy a mixed one 4: 300 tokens of 5
-// adapters, three blocks saved, 30 us without, 34 with; 1024 tokens, seven saved, 66 and 58.)
+// Whether the GEMM takes its tokens by adapter: where it saves a unit some rank blocks, if the batch is
+// mixed. Forward: six (the launch costs a sorted batch 1 us and the copy a mixed one 4: 300 tokens
+// of 5 adapters, three blocks saved, 30 us without, 34 with; 1024 tokens, seven saved, 66 and 58).
+// Backward: twelve (reading rows by the order costs the element-wise kernel 6 us of 32 at 2048 tokens:
+// 2 adapters have one block to save; 512 tokens of 48 of rank 32 save 46: 248 us without, 201 with; 2704 of 8
+// of rank 64 633 and 551, 611 and 549 if they come sorted).
 bool gated_order(const GatedPlan& plan, bool bwd, int M, int n_adapters, int r_max)
 {
-    if (bwd || plan.mt < 2) return false;
+    if (plan.mt < 2) return false;
     const int R = (r_max + 15) / 16, all = (n_adapters < M ? n_adapters : M) * R;
-    return (double)(all - (double)all / plan.mt - R) * plan.tiles / plan.units >= 6;
+    return (double)(all - (double)all / plan.mt - R) * plan.tiles / plan.units >= (bwd ? 12 : 6);
 }
 
 // A choice of tile: output columns, and the microseconds a CTA or pair takes per stage (64 of K)
@@ -1405,13 +1407,18 @@ size_t gated_expand_bytes(int M, int n_adapters, int r_max)
     return most;
 }
 
+bool gated_by_adapter(bool backward, int M, const lora_pool_t& pool, bool save)
+{
+    return gated_order(gated_plan(backward, M, pool.h_in, pool.h_out, save), backward, M, pool.n_adapters, pool.r_max);
+}
+
 size_t gated_gather_bytes(int M, int K) { return M > kGTileM ? (size_t)M * K * 2 : 0; }
 
 cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
                                 cudaStream_t stream)
 {
     const int K = pool.h_in;
-    if (!gated_order(gated_plan(false, M, K, pool.h_out, save), false, M, pool.n_adapters, pool.r_max)) return cudaSuccess;
+    if (!gated_by_adapter(false, M, pool, save)) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((M + kGatherRows - 1) / kGatherRows), (unsigned)((K + kGatherCols - 1) / kGatherCols), 1);
     cfg.blockDim = dim3(kGatherThreads, 1, 1);

@@ -31,6 +31,7 @@ struct PointParams {
     const uint16_t* dh;
     const uint8_t *g_codes, *g_scales, *u_codes, *u_scales;
     uint16_t *dg, *du, *h;
+    const int32_t* order;  // dg's and du's rows are these tokens (NULL: the tokens as they come)
     int* count;  // count_words words to zero
     int count_words, F;
     uint32_t tasks, segs;
@@ -51,7 +52,7 @@ __device__ __forceinline__ void act_and_slope(float g, float& a, float& d)
     }
 }
 
-template <int ACT, bool H>
+template <int ACT, bool H, bool ORDER>
 __global__ void __launch_bounds__(kEThreads)
 gated_point_kernel(const PointParams p)
 {
@@ -64,8 +65,15 @@ gated_point_kernel(const PointParams p)
         uint4 dh[kEInFlight];
         uint2 gc[kEInFlight], uc[kEInFlight];
         uint32_t gE[kEInFlight], uE[kEInFlight];
-        size_t at[kEInFlight];
+        size_t at[kEInFlight], to[kEInFlight];
         bool live[kEInFlight];
+        uint32_t tok[kEInFlight];
+#pragma unroll
+        for (int i = 0; i < kEInFlight; ++i) {
+            const uint64_t t = t0 + (uint64_t)i * stride;
+            tok[i] = t < p.tasks ? (uint32_t)t / p.segs : 0;
+            if (ORDER) tok[i] = (uint32_t)p.order[tok[i]];
+        }
 #pragma unroll
         for (int i = 0; i < kEInFlight; ++i) {
             const uint64_t t = t0 + (uint64_t)i * stride;
@@ -75,8 +83,9 @@ gated_point_kernel(const PointParams p)
                 const int col = (int)((uint32_t)t - row * p.segs) * kETaskCols + lane * 8;
                 if (col < p.F) {
                     live[i] = true;
-                    at[i] = (size_t)row * p.F + col;
-                    const size_t sc = (size_t)row * nb + (col >> 5);
+                    to[i] = (size_t)row * p.F + col;
+                    at[i] = (size_t)tok[i] * p.F + col;
+                    const size_t sc = (size_t)tok[i] * nb + (col >> 5);
                     dh[i] = __ldcs(reinterpret_cast<const uint4*>(p.dh + at[i]));
                     gc[i] = __ldcs(reinterpret_cast<const uint2*>(p.g_codes + at[i]));
                     uc[i] = __ldcs(reinterpret_cast<const uint2*>(p.u_codes + at[i]));
@@ -109,8 +118,8 @@ gated_point_kernel(const PointParams p)
                 ou[e] = pack_bf16x2(dy[0] * a[0], dy[1] * a[1]);
                 oh[e] = pack_bf16x2(a[0] * u[0], a[1] * u[1]);
             }
-            *reinterpret_cast<uint4*>(p.dg + at[i]) = make_uint4(og[0], og[1], og[2], og[3]);
-            *reinterpret_cast<uint4*>(p.du + at[i]) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            *reinterpret_cast<uint4*>(p.dg + to[i]) = make_uint4(og[0], og[1], og[2], og[3]);
+            *reinterpret_cast<uint4*>(p.du + to[i]) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
             if (H) *reinterpret_cast<uint4*>(p.h + at[i]) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
         }
     }
@@ -159,26 +168,28 @@ __device__ __forceinline__ uint32_t o_chunk(int t, int c)
     return (uint32_t)(t * CH * 16 + ((c ^ (t & 7)) << 4));
 }
 
-// T tokens per step.
-template <int R16, int T>
-__global__ void __launch_bounds__(kOThreads)
-gated_outer_kernel(const OuterParams p)
+// T tokens per step. LONG: dA's side. BY_ADAPTER: the operands' rows and d's are in the segments' order.
+// (Where the rows lie is fixed at compile time: 2704 tokens of 8 adapters of rank 64 take 104 us so, 169
+// with every row looked up, 214 with rows that depend on the side at run time.)
+template <int R16, int T, bool LONG, bool BY_ADAPTER>
+__device__ __forceinline__ void outer_sums(const OuterParams& p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kOpCh = R16 / 4;               // 16-byte chunks of an operand row (hi and lo)
     constexpr int kLngBytes = T * kOL * 2, kOpBytes = T * kOpCh * 16, kStage = kLngBytes + kOpBytes;
     constexpr int NT = R16 / 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
-    const bool long_rows = (int)blockIdx.x < p.a_blocks;
-    const OuterSide& d = long_rows ? p.a : p.b;
-    const int lb0 = ((int)blockIdx.x - (long_rows ? 0 : p.a_blocks)) * p.run, a = (int)blockIdx.y, s = (int)blockIdx.z;
+    const OuterSide& d = LONG ? p.a : p.b;
+    const int lb0 = ((int)blockIdx.x - (LONG ? 0 : p.a_blocks)) * p.run, a = (int)blockIdx.y, s = (int)blockIdx.z;
     const int blocks = min(p.run, (d.L + kOL - 1) / kOL - lb0);
     const int t0 = p.indptr[a], n_tok = p.indptr[a + 1] - t0;
     const int r = max(1, min(p.ranks ? p.ranks[a] : p.r_max, p.r_max));
     const uint16_t* lng = d.lng + (size_t)s * d.lng_slice;
     const uint16_t* ops = d.ops + (size_t)s * p.M * (2 * R16);
+    // rows of the segments' positions
+    const int32_t* perm = p.perm + t0;
+    auto l_row = [&](int t) { return (size_t)(LONG || !BY_ADAPTER ? perm[t] : t0 + t); };
+    auto op_row = [&](int t) { return (size_t)(BY_ADAPTER ? t0 + t : perm[t]); };
     const uint32_t base = ptx::smem_u32(smem);
     const int steps = (n_tok + T - 1) / T;
     const int i8 = lane >> 3, rr = lane & 7;
@@ -204,7 +215,7 @@ gated_outer_kernel(const OuterParams p)
             for (int h = 0; h < 2; ++h) {
                 const int l = warp * 16 + g + h * 8;
                 const uint32_t v = pack_bf16x2(j < r ? acc[n][2 * h] : 0.f, j + 1 < r ? acc[n][2 * h + 1] : 0.f);
-                if (long_rows) {
+                if (LONG) {
                     *reinterpret_cast<uint32_t*>(o + l * kPitchA + j) = v;
                 } else {
                     o[j * kPitchB + l] = (uint16_t)(v & 0xffffu);
@@ -213,7 +224,7 @@ gated_outer_kernel(const OuterParams p)
             }
         }
         __syncthreads();
-        if (long_rows) {  // [64][r_max], one run of memory
+        if (LONG) {  // [64][r_max], one run of memory
             const int pieces = p.r_max >> 3, lg = __ffs(pieces) - 1;
             uint16_t* out = d.out + (((size_t)s * p.n_adapters + a) * d.L + l0) * p.r_max;
             for (int idx = tid; idx < kOL * pieces; idx += kOThreads) {
@@ -236,7 +247,7 @@ gated_outer_kernel(const OuterParams p)
 #pragma unroll
         for (int i = 0; i < T * 8 / kOThreads; ++i) {
             const int t = (tid >> 3) + i * (kOThreads / 8);
-            rows[i] = t < n_tok ? lng + (size_t)p.perm[t0 + t] * d.L + (tid & 7) * 8 : nullptr;
+            rows[i] = t < n_tok ? lng + l_row(t) * d.L + (tid & 7) * 8 : nullptr;
         }
         auto fetch = [&](int b) {
             if (b < blocks) {
@@ -254,7 +265,7 @@ gated_outer_kernel(const OuterParams p)
         for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
             const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh;
             const bool in = t < n_tok;
-            const uint16_t* src = in ? ops + (size_t)p.perm[t0 + t] * (2 * R16) + c * 8 : ops;
+            const uint16_t* src = in ? ops + op_row(t) * (2 * R16) + c * 8 : ops;
             ptx::cp_async16(base + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
         }
         for (int k = 0; k < kOStages - 1; ++k) fetch(k);
@@ -299,14 +310,14 @@ gated_outer_kernel(const OuterParams p)
                 for (int i = 0; i < T * (kOL / 8) / kOThreads; ++i) {
                     const int idx = tid + i * kOThreads, t = idx >> 3, c = idx & 7, pos = step * T + t;
                     const bool in = pos < n_tok && l0 + c * 8 < d.L;
-                    const uint16_t* src = in ? lng + (size_t)p.perm[t0 + pos] * d.L + l0 + c * 8 : lng;
+                    const uint16_t* src = in ? lng + l_row(pos) * d.L + l0 + c * 8 : lng;
                     ptx::cp_async16(st + o_chunk<8>(t, c), src, in ? 16 : 0);
                 }
 #pragma unroll
                 for (int i = 0; i < T * kOpCh / kOThreads; ++i) {
                     const int idx = tid + i * kOThreads, t = idx / kOpCh, c = idx % kOpCh, pos = step * T + t;
                     const bool in = pos < n_tok;
-                    const uint16_t* src = in ? ops + (size_t)p.perm[t0 + pos] * (2 * R16) + c * 8 : ops;
+                    const uint16_t* src = in ? ops + op_row(pos) * (2 * R16) + c * 8 : ops;
                     ptx::cp_async16(st + kLngBytes + o_chunk<kOpCh>(t, c), src, in ? 16 : 0);
                 }
             }
@@ -341,6 +352,16 @@ gated_outer_kernel(const OuterParams p)
     }
 }
 
+template <int R16, int T, bool BY_ADAPTER>
+__global__ void __launch_bounds__(kOThreads)
+gated_outer_kernel(const OuterParams p)
+{
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    if ((int)blockIdx.x < p.a_blocks) outer_sums<R16, T, true, BY_ADAPTER>(p);
+    else outer_sums<R16, T, false, BY_ADAPTER>(p);
+}
+
 // ------------------------------------------------------------------ shrink
 //
 // v[t][j] = sum_l lng[t][l] w[l][j] for both slices: x.A_a (w's rows are l, as A is stored) and
@@ -358,6 +379,7 @@ struct ShrinkSide {
     float* v;           // [planes][2][M][r_max]
     int L, planes, steps;  // steps of 64 per plane
     bool down;
+    bool by_adapter;  // lng's rows are in the segments' order
 };
 constexpr int kScanPer = 4;  // scanning CTAs per plane
 static_assert(8 * kScanPer <= kGatedScanMax, "marks of a scan's parts");
@@ -430,7 +452,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const ShrinkS
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = (tid >> 3) + 16 * i;
-        rows[i] = t < n_tok ? lng + (size_t)p.perm[tl.y + t] * d.L : nullptr;
+        rows[i] = t < n_tok ? lng + (size_t)(d.by_adapter ? tl.y + t : p.perm[tl.y + t]) * d.L : nullptr;
     }
     auto fetch = [&](int k) {
         if (k < k1) {
@@ -601,11 +623,11 @@ cudaError_t launch_shrink(const ShrinkParams& p, int sides, int rows, cudaStream
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int R16, int T>
+template <int R16, int T, bool BY_ADAPTER>
 cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 {
     const size_t smem = (size_t)kOStages * (T * kOL * 2 + T * R16 * 4) + (size_t)(R16 + 8) * (kOL + 8) * 2;
-    auto kern = gated_outer_kernel<R16, T>;
+    auto kern = gated_outer_kernel<R16, T, BY_ADAPTER>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -623,21 +645,33 @@ cudaError_t launch_outer(const OuterParams& p, cudaStream_t stream)
 
 // Few tokens per adapter: short steps, whose buffers let more CTAs run on an SM, and several blocks per
 // CTA, so that the next block's rows arrive while one is finished.
-template <int R16>
+template <int R16, bool BY_ADAPTER>
 cudaError_t launch_outer(OuterParams& p, cudaStream_t stream)
 {
     const bool few = p.M <= 32LL * p.n_adapters;
     p.run = few ? 4 : 1;
     p.a_blocks = ((p.a.L + kOL - 1) / kOL + p.run - 1) / p.run;
-    return few ? launch_outer<R16, 32>(p, stream) : launch_outer<R16, 64>(p, stream);
+    return few ? launch_outer<R16, 32, BY_ADAPTER>(p, stream) : launch_outer<R16, 64, BY_ADAPTER>(p, stream);
+}
+template <int R16>
+cudaError_t launch_outer(OuterParams& p, bool by_adapter, cudaStream_t stream)
+{
+    return by_adapter ? launch_outer<R16, true>(p, stream) : launch_outer<R16, false>(p, stream);
+}
+
+template <int ACT, bool H>
+cudaError_t launch_point(const cudaLaunchConfig_t& cfg, const PointParams& p)
+{
+    return p.order ? cudaLaunchKernelEx(&cfg, gated_point_kernel<ACT, H, true>, p) : cudaLaunchKernelEx(&cfg, gated_point_kernel<ACT, H, false>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
-                               void* dg, void* du, void* h, int* count, cudaStream_t stream)
+                               const int32_t* order, void* dg, void* du, void* h, int* count, cudaStream_t stream)
 {
     PointParams p = {};
+    p.order = order;
     p.count = count;
     p.count_words = (int)(gated_count_bytes() / 4);  // at most a CTA's threads
     p.dh = static_cast<const uint16_t*>(dh);
@@ -662,11 +696,8 @@ cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (act == LORA_ACT_SILU)
-        return h ? cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_SILU, true>, p)
-                 : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_SILU, false>, p);
-    return h ? cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, true>, p)
-             : cudaLaunchKernelEx(&cfg, gated_point_kernel<LORA_ACT_GELU, false>, p);
+    if (act == LORA_ACT_SILU) return h ? launch_point<LORA_ACT_SILU, true>(cfg, p) : launch_point<LORA_ACT_SILU, false>(cfg, p);
+    return h ? launch_point<LORA_ACT_GELU, true>(cfg, p) : launch_point<LORA_ACT_GELU, false>(cfg, p);
 }
 
 // Parts of L: about four CTAs per SM, at most eight planes, at least four steps of 64 each.
@@ -699,6 +730,7 @@ cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora
     for (int i = 0; i < n; ++i) {
         ShrinkSide& d = p.side[i];
         d.down = sides[i].down;
+        d.by_adapter = sides[i].by_adapter;
         d.lng = static_cast<const uint16_t*>(sides[i].lng);
         d.lng_slice = sides[i].lng_slice;
         d.w = static_cast<const uint16_t*>(d.down ? pool.A : pool.B);
@@ -731,9 +763,10 @@ cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora
 }
 
 cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
-                               const lora_pool_t& pool, const lora_segments_t& seg, cudaStream_t stream)
+                               const lora_pool_t& pool, const lora_segments_t& seg, bool by_adapter, cudaStream_t stream)
 {
     OuterParams p = {};
+    p.perm = seg.perm;
     p.a.lng = static_cast<const uint16_t*>(x);
     p.a.ops = static_cast<const uint16_t*>(ops_u);
     p.a.out = static_cast<uint16_t*>(dA);
@@ -743,15 +776,14 @@ cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const
     p.b.ops = static_cast<const uint16_t*>(ops_v);
     p.b.out = static_cast<uint16_t*>(dB);
     p.b.L = pool.h_out;
-    p.perm = seg.perm;
     p.indptr = seg.indptr;
     p.ranks = pool.ranks;
     p.M = M;
     p.n_adapters = pool.n_adapters;
     p.r_max = pool.r_max;
-    if (pool.r_max <= 16) return launch_outer<16>(p, stream);
-    if (pool.r_max == 32) return launch_outer<32>(p, stream);
-    return launch_outer<64>(p, stream);
+    if (pool.r_max <= 16) return launch_outer<16>(p, by_adapter, stream);
+    if (pool.r_max == 32) return launch_outer<32>(p, by_adapter, stream);
+    return launch_outer<64>(p, by_adapter, stream);
 }
 
 }  // namespace lora

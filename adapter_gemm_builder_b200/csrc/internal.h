@@ -83,6 +83,7 @@ struct GatedSide {
     bool down;
     const void* lng;
     int64_t lng_slice;
+    bool by_adapter;  // lng's rows are in the segments' order
     float* v;
     void* ops;  // where launch_gated_operands puts the side's operands
 };
@@ -127,12 +128,16 @@ struct GatedGemmArgs {
 cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream);
 // dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu).
 // Also zeroes `count` (gated_count_bytes).
+// order: NULL, or the tokens of dg's and du's rows.
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
-                               void* dg, void* du, void* h, int* count, cudaStream_t stream);
+                               const int32_t* order, void* dg, void* du, void* h, int* count, cudaStream_t stream);
+// Whether the GEMM's rows are the tokens in the segments' order (gated.cu). by_adapter below: so are
+// d's and the operands'.
+bool gated_by_adapter(bool backward, int M, const lora_pool_t& pool, bool save);
 // Gradients of both slices, bf16: dA[s][a][k][j] = sum_t x[t][k] op_u[s][t][j] and dB[s][a][j][f] =
 // sum_t op_v[s][t][j] d[s][t][f] over the adapter's tokens.
 cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
-                               const lora_pool_t& pool, const lora_segments_t& seg, cudaStream_t stream);
+                               const lora_pool_t& pool, const lora_segments_t& seg, bool by_adapter, cudaStream_t stream);
 
 struct Fp8GemmArgs {
     int M, N, K;
