@@ -12,23 +12,25 @@
 // (one checkpoint scale) lies in one thread. Backward: the sum runs over dg then du (2F long),
 // and Wg, Wu [F][K] are read as they are, as the MMA's MN-major operand (no transposed copy).
 //
-// The LoRA term extends the sum of a tile. operand_kernel below lists, for every 128 tokens, the
-// rank blocks (16 ranks of an adapter) that any of them uses; a step adds `ups` blocks of one
+// The LoRA term extends the sum of a tile. The kernels before this one list, for every token tile, the
+// rank blocks (16 ranks of an adapter) that any of its rows uses; a step adds `ups` blocks of one
 // slice: s_a v of the tile's rows (zero in the blocks of other adapters) against the blocks of
 // B_a (forward, MN-major as it is stored) or A_a (backward, K-major as it is stored). v is split
-// into bf16 halves hi + lo that add up in the accumulator (16 bits of v). The steps have shared
-// memory of their own beside the ring and are spread between the main stages (in a CTA's first
-// tile from its second quarter on, so that the shrink runs under the first); the builders copy
-// with cp.async, one step ahead of the one that they hand over where two buffers fit. (Steps in ring
-// slots, loaded when the slot was free, had cost the ring about 2 us each: 36 tokens of 32 adapters
-// took 160 us, 37 us without them; now 53.)
-// The forward takes the tokens of more than one token tile in the segments' order, by adapter: a tile
-// then needs few adapters' blocks however the batch is mixed. gather_kernel copies x's rows into that
-// order, except where 128 of them follow one another already, as in a batch that comes sorted; h
-// and the checkpoints are written to the tokens' own rows. (2048 tokens mixed over 48 adapters of
-// rank 16: 940 us in their own order, 298 in this; over 16 of rank 64 1480, 336. TMA's gather of four
-// rows at a time took 1.2 us a stage instead of .4.)
-// The backward writes dg and du in that order to begin with (gated_order says when).
+// into bf16 halves hi + lo that add up in the accumulator (16 bits of v).
+// Forward: a step is a stage of the ring like the others. expand_kernel writes its operand out, zeros
+// included, so that it is one or two boxes; B comes by TMA from the pool. The steps lie between the main
+// stages, in a unit's first tile in the last eighth, so that the shrink runs under the others.
+// (Steps of their own buffers, put together by eight warps with cp.async, had cost 1.5 us each where
+// they were many: 512 tokens of 48 adapters of rank 32 388 us, 171 in the ring.)
+// Backward: a step has shared memory beside the ring, where builders put it together with cp.async, one
+// ahead of the one that they hand over where two buffers fit; its sums are long beside its steps.
+// The tokens of more than one token tile come in the segments' order, by adapter, where that saves
+// steps (gated_order): a tile then needs few adapters' blocks however the batch is mixed. gather_kernel
+// copies x's rows into that order, except where 128 of them follow one another already, as in a
+// batch that comes sorted; h and the checkpoints are written to the tokens' own rows. (2048 tokens
+// mixed over 48 adapters of rank 16: 940 us in their own order, 298 in this; over 16 of rank 64 1480,
+// 336. TMA's gather of four rows at a time took 1.2 us a stage instead of .4.) The backward
+// writes dg and du in that order to begin with.
 //
 // More than 128 tokens usually run on pairs of CTAs (cta_group::2, clusters of two): 256 tokens by
 // the same columns, each CTA with its 128 rows of A and half of B (forward: the even CTA the
@@ -47,9 +49,10 @@
 // shared tiles into one equal run per unit made 1024 tokens 212 us instead of 164, by reading the
 // weights at different times; in the forward, bound by power, sharing gained nothing.)
 //
-// Roles (576 threads): warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column
-// chunks by w / 4); warp 8 fills the ring by TMA; warp 9 issues the MMAs; warps 10..17 build
-// the LoRA steps. Two accumulators (512 TMEM columns), so a tile drains under the next one's
+// Roles: warps 0..7 drain accumulators (warp w: TMEM lanes 32 (w % 4), column chunks by w / 4); warp 8
+// fills the ring by TMA; warp 9 issues the MMAs; behind them the forward has four warps that fetch the
+// steps' B (448 threads), the backward eight that build its LoRA steps (576). Two accumulators
+// (512 TMEM columns), so a tile drains under the next one's
 // products. Every wait is bounded; on expiry the CTA records a status word, lets what it
 // issued land and leaves.
 #include <cuda.h>
@@ -255,6 +258,23 @@ __device__ __forceinline__ int block_rank0(int u) { return (u >> 7 & 3) * 16; }
 __device__ __forceinline__ int block_live(int u) { return u & 31; }
 __device__ __forceinline__ int block_bad(int u) { return u >> 5 & 3; }
 constexpr int kNoBlock = -3 * 512;  // an adapter that no row has, nothing live
+// The rank in column j of block b of an adapter of rank R in the forward's operand, -1: zero. A box of B's
+// rows must not reach past the rank, where the pool holds anything, so the last block of several is the
+// last 16 ranks, and a single one below 16 is its first p and its last p ranks, p the largest power of
+// two, zeros behind them. What comes twice is used once. (Boxes of the powers of two that make up the
+// rank, and zeros to 16, five or six copies: 512 tokens of 48 adapters of rank up to 32 139 us, so 135; 36
+// of 32 53.6, 52.)
+__device__ __forceinline__ int block_rank(int R, int b, int j)
+{
+    if (R >= 16) {
+        const int r = min(16 * b, R - 16) + j;
+        return r >= 16 * b ? r : -1;
+    }
+    const int p = 1 << (31 - __clz(R));
+    if (j < p) return j;
+    const int r = R - 2 * p + j;
+    return j < 2 * p && r >= p ? r : -1;
+}
 // LoRA steps of a token tile with this many rank blocks, both slices; a piece of a shared tile has
 // its share of them.
 __device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
@@ -639,22 +659,21 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                 q = job.z;
             }
             if (u != kNoBlock && lane < atoms) {
-                // the block's live rows, then zeros (past the last matrix; a marked one is zeros too, see
-                // Eight), in boxes of powers of two
+                // see block_rank; what is past the last matrix comes as zeros (a marked one too, see Eight)
                 const int x = (job.y / p.mt) * p.cols + rank * (p.cols / kCtas) + lane * 64, nothing = 2 * p.n_adapters;
                 const uint32_t dst = base_u + (uint32_t)(job.x * p.stage_bytes) + lora_b_offset(p) + (uint32_t)((lane * p.ups + k) * 2048);
-                int z = block_bad(u) >> s & 1 ? nothing : s * p.n_adapters + block_adapter(u);
-                for (int row = 0, left = block_live(u);;) {
-                    while (left) {
-                        const int b = 31 - __clz(left), y = block_rank0(u) + row;
-                        if (PAIR) ptx::tma_load_3d_pair(dst + (uint32_t)(row * 128), &maps.l[b], leaders(&full[job.x]), x, y, z);
-                        else ptx::tma_load_3d(dst + (uint32_t)(row * 128), &maps.l[b], &full[job.x], x, y, z);
-                        row += 1 << b;
-                        left -= 1 << b;
-                    }
-                    if (row == 16) break;
-                    left = 16 - row;
-                    z = nothing;
+                const int z = block_bad(u) >> s & 1 ? nothing : s * p.n_adapters + block_adapter(u), live = block_live(u);
+                auto box = [&](int row, int b, int y, int matrix) {
+                    if (PAIR) ptx::tma_load_3d_pair(dst + (uint32_t)(row * 128), &maps.l[b], leaders(&full[job.x]), x, y, matrix);
+                    else ptx::tma_load_3d(dst + (uint32_t)(row * 128), &maps.l[b], &full[job.x], x, y, matrix);
+                };
+                if (live == 16 || block_rank0(u)) {
+                    box(0, 4, block_rank0(u) + live - 16, z);
+                } else {
+                    const int b = 31 - __clz(live);
+                    box(0, b, 0, z);
+                    box(1 << b, b, live - (1 << b), z);
+                    for (int k2 = b + 1; k2 < 4; ++k2) box(1 << k2, k2, 0, nothing);
                 }
             }
             __syncwarp();
@@ -667,12 +686,12 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
             // A builder's pieces lie in one column of 16-byte pieces, a fixed number of rows apart
             // (a multiple of eight, so their swizzle is the same): piece i of the operand in row
             // a_row + i a_step, column a_c; of A_a in row b_row + i b_step (an output column), column b_c.
-            const int a_lg = p.ups == 4 ? 4 : 3, a_c = bt & ((1 << a_lg) - 1), a_row = bt >> a_lg, a_step = kGBuilders >> a_lg;
+            const int a_c = bt & 7, a_row = bt >> 3, a_step = kGBuilders >> 3;  // (two blocks per step)
             const int a_rows = p.a_bytes >> 7;
-            const int a_half = a_c >> (a_lg - 1), a_k = a_c & ((1 << (a_lg - 1)) - 1);  // hi or lo; piece of the blocks
+            const int a_half = a_c >> 2, a_k = a_c & 3;  // hi or lo; piece of the blocks
             const int b_c = bt & 3, b_row = bt >> 2, b_step = kGBuilders >> 2;
             const int b_cols = p.cols / kCtas, b_n0 = rank * b_cols;  // this CTA's columns of the tile
-            const uint32_t a_off = (uint32_t)((a_c >> 3) * p.a_bytes + a_row * 128 + (((a_c & 7) ^ (a_row & 7)) << 4));
+            const uint32_t a_off = (uint32_t)(a_row * 128 + ((a_c ^ (a_row & 7)) << 4));
             const uint32_t b_off = lora_b_offset(p) + (uint32_t)(b_row * 64 + ((b_c ^ ((b_row >> 1) & 3)) << 4));
             // the walk over the steps: step e of `ext` of the tile
             Walk w(unit);
@@ -1190,9 +1209,23 @@ expand_kernel(const OperandParams p)
         if (p.scales) scale = p.scales[a];
     }
     ptx::pdl_wait();  // from here on what the shrink wrote
+    __shared__ float s_v[2 * kOpRows][LORA_MAX_RANK + 4];
+    Eight v;
     if (live) {
-        Eight v;
         v.load(p, d.v, d.planes, s, tok, r, scale, c, marked(p, a, s));
+        if (r < p.r16) {  // ranks to their columns
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_v[mine][8 * c + e] = v.f[e];
+        }
+    }
+    __syncthreads();
+    if (live) {
+        if (r < p.r16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int k = block_rank(r, c >> 1, (c & 1) * 8 + e);
+                v.f[e] = k < 0 ? 0.f : s_v[mine][k];
+            }
         const int b = t.first[row] + (c >> 1), e = 2 * (b / p.ups) + s, piece = (b % p.ups) * 2 + (c & 1);
         *piece_at(e, piece, row) = v.half();
         *piece_at(e, 2 * p.ups + piece, row) = v.half();
@@ -1203,7 +1236,7 @@ expand_kernel(const OperandParams p)
     }
 }
 
-// LoRA step buffers beside a ring of enough stages (36 tokens of 32 adapters: one 56 us, two or three 48).
+// The backward's LoRA step buffers beside a ring of enough stages.
 int lora_buffers(const GatedParams& p, int room, bool pair)
 {
     int n = 1;

@@ -86,14 +86,25 @@ class Problem:
         return out
 
 
+def guarded(op, M, K, pool):
+    """A workspace of exactly the asked size with 64 KB of 0xff behind it."""
+    n = L.lora_workspace_size(op, M, K, pool)
+    room = torch.full((n + 65536,), 0xff, dtype=torch.uint8, device="cuda")
+    room[:n] = L.workspace(op, M, K, pool)[:n]
+    return room, room[:n]
+
+
 def forward(p, act="silu", save=False, stream=None):
     pool, seg = p.device()
     x, Wg, Wu = p.x.cuda(), p.Wg.cuda(), p.Wu.cuda()
     h = torch.full((p.M + 1, p.F), 7.0, dtype=torch.bfloat16, device="cuda")
     kept = (L.Act8(p.M, p.F), L.Act8(p.M, p.F)) if save else None
-    ws = L.workspace(L.LORA_OP_BF16_GATED, p.M, p.K, pool)
+    room, ws = guarded(L.LORA_OP_BF16_GATED, p.M, p.K, pool)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
     L.bf16_gated_gemm_lora_epilogue(x, Wg, Wu, pool, seg, h[:p.M], ws, act=ACTS[act], save=kept, stream=stream)
     torch.cuda.synchronize()
+    assert (room[ws.numel():] == 0xff).all()
     st, detail = L.lora_workspace_status(ws)
     assert st == L.LORA_OK, hex(detail)
     assert (h[p.M] == 7).all()  # the row behind the last is left alone
@@ -128,6 +139,8 @@ FORWARD = [
     (2049, 72, 3000, 9, 64, "zipf"),
     # tiles shared between CTAs: parts of a tile summed by whichever is done last
     (300, 4096, 1000, 3, 16, "zipf"), (513, 2048, 5000, 2, 32, "sorted_zipf"), (130, 8192, 272, 40, 64, "uniform"),
+    # a token tile full of different adapters, one tile and two
+    (128, 512, 1040, 128, 64, "uniform"), (256, 264, 9600, 256, 32, "uniform"),
 ]
 
 
@@ -187,10 +200,11 @@ def backward(p, act="silu", x8=False, h=False, seed=5):
         dA = torch.full((2, p.n, p.K, p.r), float("nan"), dtype=torch.bfloat16, device="cuda")
         dB = torch.full((2, p.n, p.r, p.F), float("nan"), dtype=torch.bfloat16, device="cuda")
     hb = torch.full((p.M + 1, p.F), 7.0, dtype=torch.bfloat16, device="cuda") if h else None
-    ws = L.workspace(L.LORA_OP_BF16_GATED_BACKWARD, p.M, p.F, pool)
+    room, ws = guarded(L.LORA_OP_BF16_GATED_BACKWARD, p.M, p.F, pool)
     L.bf16_gated_lora_backward(p.dh.cuda(), p.Wg.cuda(), p.Wu.cuda(), pool, seg, g8, u8, x if p.n else None, dX[:p.M],
                                dA, dB, ws, act=ACTS[act], h=hb[:p.M] if h else None)
     torch.cuda.synchronize()
+    assert (room[ws.numel():] == 0xff).all()
     st, detail = L.lora_workspace_status(ws)
     assert st == L.LORA_OK, hex(detail)
     assert (dX[p.M] == 7).all() and (not h or (hb[p.M] == 7).all())
@@ -249,6 +263,8 @@ def check_backward(p, act, o):
     # long sums: every tile shared, few tokens and many
     (1, 128, 8192, 1, 16, "identical", "silu", False, False), (20, 1040, 4112, 7, 32, "uniform", "silu", True, True),
     (300, 520, 6000, 0, 8, "uniform", "silu", False, False), (700, 1000, 3008, 6, 64, "zipf", "gelu", False, True),
+    # many adapters mixed over several tiles: rows by adapter, with shared tiles and without
+    (300, 528, 6000, 60, 16, "uniform", "silu", True, True), (520, 264, 1040, 130, 32, "zipf", "gelu", False, False),
 ])
 def test_backward(M, K, F, n, r, ids, act, x8, h):
     p = Problem(M, K, F, n, r, ids)
