@@ -60,6 +60,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstring>
 
 #include "act8.cuh"
 #include "internal.h"
@@ -119,13 +120,14 @@ struct GatedParams {
     const int32_t* tok_adapter;
     const int32_t* order;     // the token of each row of the tiles (NULL: the rows are the tokens)
     int n_adapters, r_max, r16;
-    int ups;                  // rank blocks per step
+    int ups;                  // rank blocks per step (forward: those of both slices counted)
     int lbufs, lora_bytes;    // backward: step buffers behind the ring
 };
+template <bool RING>
 struct GatedMaps {
-    CUtensorMap a[2], b[2];     // x and its rows by adapter, or dg, du; Wg, Wu
-    CUtensorMap e;              // forward: the expanded operand (expand_kernel)
-    CUtensorMap l[kRankBoxes];  // forward: the pool's B [2 n_adapters][r_max][NC]
+    CUtensorMap a[2], b[2];                // x and its rows by adapter, or dg, du; Wg, Wu
+    CUtensorMap e;                         // RING: the expanded operand (expand_kernel)
+    CUtensorMap l[RING ? kRankBoxes : 1];  // RING: the pool's B [2 n_adapters][r_max][NC]
 };
 
 // K-major operand, 128-byte rows, 128-byte swizzle: 8-row groups 1024 bytes apart.
@@ -275,9 +277,14 @@ __device__ __forceinline__ int block_rank(int R, int b, int j)
     const int r = R - 2 * p + j;
     return j < 2 * p && r >= p ? r : -1;
 }
-// LoRA steps of a token tile with this many rank blocks, both slices; a piece of a shared tile has
-// its share of them.
-__device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks) { return 2 * ((blocks + p.ups - 1) / p.ups); }
+// LoRA steps of a token tile with this many rank blocks: forward ups / 2 blocks with both slices each (one
+// block, a sorted batch's usual tile, is one stage then and not two), backward ups of one
+// slice. A piece of a shared tile has its share of them.
+template <int MODE>
+__device__ __forceinline__ int lora_steps(const GatedParams& p, int blocks)
+{
+    return MODE == kGFwd ? (blocks + p.ups / 2 - 1) / (p.ups / 2) : 2 * ((blocks + p.ups - 1) / p.ups);
+}
 __device__ __forceinline__ int steps_begin(const GatedParams& p, int steps, int piece) { return piece < 0 ? 0 : steps * piece / p.split; }
 __device__ __forceinline__ int steps_end(const GatedParams& p, int steps, int piece) { return piece < 0 ? steps : steps * (piece + 1) / p.split; }
 // A step's operand: tiles of 64 columns (four groups of 16: ups of hi, ups of lo), the B part behind
@@ -332,7 +339,7 @@ struct RowRun {
 
 template <int MODE, bool LORA, bool PAIR>
 __global__ void __launch_bounds__(MODE == kGFwd ? kGFwdThreads : kGThreads, 1)
-gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
+gated_gemm_kernel(const __grid_constant__ GatedMaps<MODE == kGFwd && LORA> maps, const GatedParams p)
 {
     constexpr bool kRing = MODE == kGFwd && LORA;  // LoRA steps come through the ring
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -341,7 +348,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
     __shared__ int s_last;       // this CTA's part of a shared tile was the last
     __shared__ uint32_t s_fills[kGMaxStages];  // PAIR: stages this CTA's producer filled, for the leader,
     __shared__ uint32_t s_tx[kGMaxStages];     // and the bytes of each one's last fill
-    __shared__ int4 s_job[2];                  // a step for the loaders: stage (-1: the end), tile, first block, slice
+    __shared__ int4 s_job[2];                  // a step for the loaders: stage (-1: the end), tile, first block
     constexpr int kCtas = PAIR ? 2 : 1, kTokens = kCtas * kGTileM;
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int unit = (int)blockIdx.x / kCtas;
@@ -505,17 +512,18 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                 base = __shfl_sync(0xffffffffu, next_base, 0);
                 fetch_list(w.tile + p.units);
                 e = 0;
-                due = lora_steps(p, blocks);
+                due = lora_steps<MODE>(p, blocks);
             };
             const int atoms = (p.cols / kCtas + 63) >> 6, rows = PAIR ? kTokens : p.a_bytes >> 7;
             auto step = [&](int e) {  // the operand; the loaders fetch B into the same stage
                 if (!stage_free()) return false;
-                hand_out(make_int4(st, w.tile, (e >> 1) * p.ups, e & 1));
+                const int first = e * (p.ups / 2);
+                hand_out(make_int4(st, w.tile, first, 0));
                 const uint32_t sa = base_u + (uint32_t)(st * p.stage_bytes);
-                expect(lora_b_offset(p) + (uint32_t)(min(p.ups, blocks - (e >> 1) * p.ups) * atoms * 2048));
+                expect(lora_b_offset(p) + (uint32_t)(min(p.ups, 2 * (blocks - first)) * atoms * 2048));
                 if (leader)
                     for (int c = 0; c < p.ups / 2; ++c)
-                        load(sa + (uint32_t)(c * p.a_bytes), &maps.e, 0, ((2 * base + e) * (p.ups / 2) + c) * rows + rank * kGTileM);
+                        load(sa + (uint32_t)(c * p.a_bytes), &maps.e, 0, ((base + e) * (p.ups / 2) + c) * rows + rank * kGTileM);
                 next_stage();
                 return true;
             };
@@ -593,7 +601,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                     blocks = p.list_len[m];
                 }
                 blocks = __shfl_sync(0xffffffffu, blocks, 0);  // uniform, and so the walk
-                const int all = lora_steps(p, blocks);
+                const int all = lora_steps<MODE>(p, blocks);
                 e = steps_begin(p, all, w.piece);
                 due = steps_end(p, all, w.piece) - e;
             };
@@ -604,11 +612,12 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                 ptx::tc_fence_after();
                 if (leader) {
                     const uint32_t at = kRing ? (uint32_t)st * stage16 : lb * ((uint32_t)p.lora_bytes >> 4);
-                    const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((e & 1) * p.cols) : d;
-                    const int n = min(p.ups, blocks - (e >> 1) * p.ups);
+                    // forward: block k / 2, slice k & 1
+                    const int n = MODE == kGFwd ? min(p.ups, 2 * (blocks - e * (p.ups / 2))) : min(p.ups, blocks - (e >> 1) * p.ups);
                     for (int h = 0; h < 2; ++h)
                         for (int k = 0; k < n; ++k) {
                             const int c = h * p.ups + k;  // 16-column group of the operand: 4 per swizzle row
+                            const uint32_t ds = MODE == kGFwd ? d + (uint32_t)((k & 1) * p.cols) : d;
                             mma(ds, la0 + at + (uint32_t)((c >> 2) * (p.a_bytes >> 4) + (c & 3) * 2),
                                 lb0 + at + (uint32_t)(k * (MODE == kGFwd ? 128 : 2)), id_lora, 1u);
                         }
@@ -641,7 +650,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
         // A warp per block of a step, since issuing copies of changing shapes is what takes time (by the
         // producer's lanes alone a step took 1 us, which was all that 64 tokens of 64 adapters of rank
         // 64 waited for: 169 us, 148 with the loaders).
-        const int k = warp - kGBuilder0, atoms = (p.cols / kCtas + 63) >> 6;
+        const int k = warp - kGBuilder0, s = k & 1, atoms = (p.cols / kCtas + 63) >> 6;
         int m = -1, q = 0, u = 0, ahead = 0;  // this warp's block of the last step, of the one after it
         for (int jobs = 0;; ++jobs) {
             ptx::named_sync(1, (1 + kGLoaders) * 32);
@@ -649,15 +658,13 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
             if (job.x < 0) break;
             if (jobs == 0) ptx::pdl_wait();
             if (k >= p.ups) continue;
-            const int jm = job.y % p.mt, s = job.w;
-            if (jm != m || job.z != q) {
-                const int32_t* list = p.lists + (size_t)jm * kListMax * kCtas + job.z + k;
-                const int left = p.list_len[jm] - job.z - k;  // blocks from this one on
-                u = left <= 0 ? kNoBlock : jm == m && job.z == q + p.ups ? ahead : list[0];
-                ahead = left > p.ups ? list[p.ups] : kNoBlock;
-                m = jm;
-                q = job.z;
-            }
+            const int jm = job.y % p.mt, per = p.ups / 2;
+            const int32_t* list = p.lists + (size_t)jm * kListMax * kCtas + job.z + (k >> 1);
+            const int left = p.list_len[jm] - job.z - (k >> 1);  // blocks from this one on
+            u = left <= 0 ? kNoBlock : jm == m && job.z == q + per ? ahead : list[0];
+            ahead = left > per ? list[per] : kNoBlock;
+            m = jm;
+            q = job.z;
             if (u != kNoBlock && lane < atoms) {
                 // see block_rank; what is past the last matrix comes as zeros (a marked one too, see Eight)
                 const int x = (job.y / p.mt) * p.cols + rank * (p.cols / kCtas) + lane * 64, nothing = 2 * p.n_adapters;
@@ -704,7 +711,7 @@ gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p)
                     n0 = (w.tile / p.mt) * p.cols + b_n0;
                     row0 = m * kTokens + rank * kGTileM;
                     blocks = p.list_len[m];
-                    const int all = lora_steps(p, blocks);
+                    const int all = lora_steps<MODE>(p, blocks);
                     ext = steps_end(p, all, w.piece);
                     e = steps_begin(p, all, w.piece) - 1;
 #pragma unroll
@@ -1160,11 +1167,11 @@ operand_kernel(const OperandParams p)
 }
 
 // Forward: the operand as the GEMM's steps have it, zeros in the blocks of other adapters written out,
-// so that a step is a few boxes of the GEMM's ring: step e (slice e & 1) of a tile is ups / 2
-// arrays [rows][64] of bf16, four groups of 16 columns each (ups of hi, ups of lo), from array
-// (2 base + e) ups / 2 on. The bases grow by what the tiles before can need at most: tokens that
-// come by adapter have (adapters before the tile's first + tiles before it) R blocks at most, R =
-// ceil(r_max / 16); in the caller's order every tile may need per_tile steps.
+// so that a step is a few boxes of the GEMM's ring: step e of a tile is ups / 2 arrays [rows][64] of
+// bf16, four groups of 16 columns each (ups of hi, ups of lo; of ups the group of block k / 2 and
+// slice k & 1), from array (base + e) ups / 2 on. The bases grow by what the tiles before can need at
+// most: tokens that come by adapter have (adapters before the tile's first + tiles before it) R blocks
+// at most, R = ceil(r_max / 16); in the caller's order every tile may need per_tile steps.
 __global__ void __launch_bounds__(kOpThreads)
 expand_kernel(const OperandParams p)
 {
@@ -1174,26 +1181,27 @@ expand_kernel(const OperandParams p)
     const int tid = threadIdx.x, per = p.tile / kOpRows, m = (int)blockIdx.x / per, row0 = (int)blockIdx.x % per * kOpRows;
     if (m * p.tile + row0 >= p.M) return;
     const bool first = tile_blocks(p, m, t);
+    const int per_step = p.ups / 2;  // blocks, of both slices
     if (p.per_tile < 0) {
         int before = 0;  // adapters with tokens before the tile's first
         for (int a0 = 0; a0 < t.id[0]; a0 += kOpThreads) {
             const int a = a0 + tid;
             before += __syncthreads_count(a < t.id[0] && p.indptr[a + 1] > p.indptr[a]);
         }
-        if (tid == 0) s_base = ((before + m) * (p.r16 >> 4) + (p.ups - 1) * m) / p.ups;
+        if (tid == 0) s_base = ((before + m) * (p.r16 >> 4) + (per_step - 1) * m) / per_step;
     } else if (tid == 0) {
         s_base = m * p.per_tile;
     }
     __syncthreads();
     const auto& d = p.side[0];
-    const int base = s_base, steps = 2 * ((t.total + p.ups - 1) / p.ups), lg = p.ups == 4 ? 4 : 3;
+    const int base = s_base, steps = (t.total + per_step - 1) / per_step, lg = p.ups == 4 ? 4 : 3;
     // where a 16-byte piece of a step's row is: groups of 16 columns, four to an array
     auto piece_at = [&](int e, int piece, int row) {
-        return reinterpret_cast<uint4*>(d.ops) + (((size_t)(2 * base + e) * (p.ups >> 1) + (piece >> 3)) * p.rows + row) * 8 + (piece & 7);
+        return reinterpret_cast<uint4*>(d.ops) + (((size_t)(base + e) * per_step + (piece >> 3)) * p.rows + row) * 8 + (piece & 7);
     };
     for (int i = tid; i < steps * kOpRows << lg; i += kOpThreads) {
         const int piece = i & ((1 << lg) - 1), row = row0 + ((i >> lg) & (kOpRows - 1)), e = (i >> lg) / kOpRows;
-        const int b = (e >> 1) * p.ups + ((piece >> 1) & (p.ups - 1)) - t.first[row];
+        const int b = e * per_step + (((piece >> 1) & (p.ups - 1)) >> 1) - t.first[row];
         if (m * p.tile + row < p.M && (b < 0 || b >= t.count[row])) *piece_at(e, piece, row) = make_uint4(0u, 0u, 0u, 0u);
     }
     // this thread's eight ranks of a row and slice
@@ -1226,7 +1234,7 @@ expand_kernel(const OperandParams p)
                 const int k = block_rank(r, c >> 1, (c & 1) * 8 + e);
                 v.f[e] = k < 0 ? 0.f : s_v[mine][k];
             }
-        const int b = t.first[row] + (c >> 1), e = 2 * (b / p.ups) + s, piece = (b % p.ups) * 2 + (c & 1);
+        const int b = t.first[row] + (c >> 1), e = b / per_step, piece = ((b - e * per_step) * 2 + s) * 2 + (c & 1);
         *piece_at(e, piece, row) = v.half();
         *piece_at(e, 2 * p.ups + piece, row) = v.half();
     }
@@ -1245,7 +1253,7 @@ int lora_buffers(const GatedParams& p, int room, bool pair)
 }
 
 template <int MODE, bool LORA, bool PAIR>
-cudaError_t launch_mode(const GatedMaps& maps, const GatedParams& p, int grid, cudaStream_t stream)
+cudaError_t launch_mode(const GatedMaps<true>& all, const GatedParams& p, int grid, cudaStream_t stream)
 {
     auto kern = gated_gemm_kernel<MODE, LORA, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
@@ -1264,6 +1272,8 @@ cudaError_t launch_mode(const GatedMaps& maps, const GatedParams& p, int grid, c
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
+    GatedMaps<MODE == kGFwd && LORA> maps;
+    memcpy(&maps, &all, sizeof(maps));
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
@@ -1396,17 +1406,18 @@ size_t gated_list_bytes(int M)
 
 namespace {
 
-// Steps per slice that expand_kernel's bases may reach, for tiles of `tile` tokens.
+// Steps that expand_kernel's bases may reach, for tiles of `tile` tokens.
 size_t gated_steps(int M, int tile, int ups, bool order, int n_adapters, int r_max)
 {
     const size_t mt = (size_t)(M + tile - 1) / tile, R = (size_t)(r_max + 15) / 16;
     const size_t all = n_adapters < M ? n_adapters : M, in_tile = all < (size_t)tile ? all : (size_t)tile;
-    if (!order) return mt * ((in_tile * R + ups - 1) / ups);
-    return ((all + mt) * R + (ups - 1) * mt) / ups + 1;
+    const size_t per_step = ups / 2;  // blocks
+    if (!order) return mt * ((in_tile * R + per_step - 1) / per_step);
+    return ((all + mt) * R + (per_step - 1) * mt) / per_step + 1;
 }
 // Rows of a step's arrays, and their bytes in the ring.
 int gated_a_rows(int M) { return M >= kGTileM ? kGTileM : (M + 7) / 8 * 8; }
-// The forward's rank blocks per step and its ring's stage, where a step has to fit: four with few tokens
+// The forward's rank blocks per step (both slices counted) and its ring's stage, where a step has to fit: four with few tokens
 // (whose operand is short) or where that much is free in a stage, else two.
 struct FwdSteps {
     int ups, stage;
@@ -1433,7 +1444,7 @@ size_t gated_expand_bytes(int M, int n_adapters, int r_max)
         const int few = (int)((2 * (6 + R)) / R + 1), kept = M > tile && n_adapters > few ? few : n_adapters;
         for (int ups = 2; ups <= 4; ups += 2) {
             const size_t a = gated_steps(M, tile, ups, false, kept, r_max), b = gated_steps(M, tile, ups, true, n_adapters, r_max);
-            const size_t bytes = (a > b ? a : b) * 2 * (ups / 2) * rows * 128;
+            const size_t bytes = (a > b ? a : b) * (ups / 2) * rows * 128;
             if (bytes > most) most = bytes;
         }
     }
@@ -1577,7 +1588,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
     }
-    GatedMaps maps;
+    GatedMaps<true> maps;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     bool ok = true;
@@ -1590,7 +1601,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
     if (a.lora && !bwd) {
         const size_t rows = plan.pair ? 2 * kGTileM : a_rows;
         const size_t steps = gated_steps(a.M, plan.pair ? 2 * kGTileM : kGTileM, p.ups, p.order != nullptr, a.n_adapters, a.r_max);
-        ok = ok && encode_tmap_2d(&maps.e, dt, a.ops, 64, steps * 2 * (p.ups / 2) * rows, 128, 64, (uint32_t)a_rows, sw);
+        ok = ok && encode_tmap_2d(&maps.e, dt, a.ops, 64, steps * (p.ups / 2) * rows, 128, 64, (uint32_t)a_rows, sw);
         const uint64_t dims[3] = {(uint64_t)a.F, (uint64_t)a.r_max, (uint64_t)(2 * a.n_adapters)};
         const uint64_t strides[2] = {(uint64_t)a.F * 2, (uint64_t)a.F * a.r_max * 2};
         for (int b = 0; b < kRankBoxes; ++b) {
