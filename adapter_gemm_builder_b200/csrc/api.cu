@@ -169,12 +169,12 @@ GatedBwdWs gated_bwd_ws(int M, int F, const lora_pool_t* pool)
 }
 
 // v = x.A (down) or d.B^T of both slices of each side, then its operands and the token tiles' rank blocks.
-cudaError_t gated_operands(const GatedSide* sides, int n, bool backward, bool save, const lora_pool_t& pool,
+cudaError_t gated_operands(const GatedPlan& plan, const GatedSide* sides, int n, bool backward, const lora_pool_t& pool,
                            const lora_segments_t& seg, int M, uint8_t* bad, void* lists, cudaStream_t s)
 {
     const cudaError_t e = launch_gated_shrink(sides, n, M, pool, seg, bad, s);
     if (e != cudaSuccess) return e;
-    return launch_gated_operands(sides, n, M, pool, seg, bad, backward, save, lists, s);
+    return launch_gated_operands(plan, sides, n, M, pool, seg, bad, backward, lists, s);
 }
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
@@ -664,10 +664,11 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
     a.g8 = g8;
     a.u8 = u8;
     a.status = reinterpret_cast<uint32_t*>(w);
+    const GatedPlan plan = gated_plan(false, M, K, F, g8 != nullptr, pool);
     if (pool) {
         const GatedSide side = {true, x, 0, false, reinterpret_cast<float*>(w + l.v), w + l.ops};
-        if (launch_gated_gather(x, M, *pool, *seg, g8 != nullptr, w + l.rows, s) != cudaSuccess) return LORA_ERR_CUDA;
-        if (gated_operands(&side, 1, false, g8 != nullptr, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+        if (launch_gated_gather(plan, x, M, K, *seg, w + l.rows, s) != cudaSuccess) return LORA_ERR_CUDA;
+        if (gated_operands(plan, &side, 1, false, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
         a.lora = true;
         a.a[1] = w + l.rows;
         a.ops = w + l.ops;
@@ -678,7 +679,7 @@ int bf16_gated_gemm_lora_epilogue(const void* x, int M, int K, int F, const void
         a.n_adapters = pool->n_adapters;
         a.r_max = pool->r_max;
     }
-    return cuda_status(launch_gated_gemm(a, s));
+    return cuda_status(launch_gated_gemm(plan, a, s));
 }
 
 int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* dh, int M, int K, int F, const void* Wg,
@@ -705,7 +706,8 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     uint16_t* du = dg + (size_t)M * F;
     // 1. dg, du (and h) from the checkpoints
     int* count = reinterpret_cast<int*>(w + l.count);
-    const bool by_adapter = pool && gated_by_adapter(true, M, *pool, false);
+    const GatedPlan plan = gated_plan(true, M, K, F, false, pool);
+    const bool by_adapter = plan.by_adapter;
     if (launch_gated_point(dh, M, F, act, *g8, *u8, by_adapter ? seg->perm : nullptr, dg, du, h, count, s) != cudaSuccess) return LORA_ERR_CUDA;
     GatedGemmArgs a = {};
     a.backward = true;
@@ -720,7 +722,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.status = reinterpret_cast<uint32_t*>(w);
     a.part = reinterpret_cast<float*>(w + l.part);
     a.count = count;
-    if (!pool) return cuda_status(launch_gated_gemm(a, s));
+    if (!pool) return cuda_status(launch_gated_gemm(plan, a, s));
     // 2. u = d.B^T and v = x.A of both slices
     if (x8) {
         if (launch_act8_expand(*x8, M, K, w + l.x, s) != cudaSuccess) return LORA_ERR_CUDA;
@@ -728,7 +730,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     }
     const GatedSide sides[2] = {{false, dg, (int64_t)M * F, by_adapter, reinterpret_cast<float*>(w + l.u), w + l.ops_u},
                                 {true, x, 0, false, reinterpret_cast<float*>(w + l.v), w + l.ops_v}};
-    if (gated_operands(sides, 2, true, false, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
+    if (gated_operands(plan, sides, 2, true, *pool, *seg, M, w + l.bad, w + l.lists, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 3. dX, the adapters' term in its sum
     a.lora = true;
     a.ops = w + l.ops_u;
@@ -738,7 +740,7 @@ int bf16_gated_lora_backward(const void* x, const lora_act8_t* x8, const void* d
     a.order = seg->perm;
     a.n_adapters = pool->n_adapters;
     a.r_max = pool->r_max;
-    if (launch_gated_gemm(a, s) != cudaSuccess) return LORA_ERR_CUDA;
+    if (launch_gated_gemm(plan, a, s) != cudaSuccess) return LORA_ERR_CUDA;
     // 4. the adapters' gradients
     return cuda_status(launch_gated_outer(x, w + l.ops_u, dA, dg, w + l.ops_v, dB, M, *pool, *seg, by_adapter, s));
 }

@@ -1017,7 +1017,8 @@ struct OperandParams {
 };
 
 constexpr int kOpThreads = 256;
-constexpr int kOpRows = 16;   // tokens per CTA
+constexpr int kOpRows = 16;   // tokens per CTA: a thread has eight ranks of one of them
+static_assert(2 * kOpRows * (LORA_MAX_RANK / 8) <= kOpThreads, "one piece per thread");
 constexpr int kPlanesMax = 8;
 
 // Whether the matrix of adapter a and slice s was marked as non-finite.
@@ -1051,6 +1052,7 @@ __device__ __forceinline__ bool tile_blocks(const OperandParams& p, int m, TileB
     t.id[tid] = id;
     __syncthreads();
     int f = tid;  // the first row of the same adapter
+#pragma unroll 8
     for (int j = (tid & ~3) - 4; j >= 0; j -= 4) {
         const int4 o = *reinterpret_cast<const int4*>(t.id + j);
         f = o.x == id ? j : o.y == id ? j + 1 : o.z == id ? j + 2 : o.w == id ? j + 3 : f;
@@ -1147,18 +1149,25 @@ operand_kernel(const OperandParams p)
     ptx::pdl_launch_dependents();
     const int tid = threadIdx.x, per = p.tile / kOpRows, m = (int)blockIdx.x / per;
     const bool lists = !blockIdx.y && (int)blockIdx.x % per == 0;  // one CTA of the tile makes its list
-    const bool first = lists && tile_blocks(p, m, t);
-    ptx::pdl_wait();
+    // this thread's eight ranks of a row and slice
     const auto& d = p.side[blockIdx.y];
-    const int chunks = p.r16 >> 3, items = 2 * kOpRows * chunks;
-    for (int i = tid; i < items; i += kOpThreads) {
-        const int c = i % chunks, rs = i / chunks, s = rs / kOpRows;
-        const int row = (int)blockIdx.x * kOpRows + rs % kOpRows;
-        if (row >= p.M) continue;
-        const int tok = p.order ? p.order[row] : row, a = p.tok_adapter[tok];
-        if (a < 0 || a >= p.n_adapters) continue;  // nobody reads these rows
+    const int chunks = p.r16 >> 3, c = tid % chunks, rs = tid / chunks, s = rs & 1, row = (int)blockIdx.x * kOpRows + (rs >> 1);
+    int a = -1, tok = 0, r = 0;
+    float scale = 1.f;
+    if (rs < 2 * kOpRows && row < p.M) {
+        tok = p.order ? p.order[row] : row;
+        a = p.tok_adapter[tok];
+        if (a >= p.n_adapters) a = -1;
+        if (a >= 0) {  // (nobody reads the other rows)
+            r = rank_of(p, a);
+            if (p.scales) scale = p.scales[a];
+        }
+    }
+    const bool first = lists && tile_blocks(p, m, t);
+    ptx::pdl_wait();  // from here on what the shrink wrote
+    if (a >= 0) {
         Eight v;
-        v.load(p, d.v, d.planes, s, tok, rank_of(p, a), p.scales ? p.scales[a] : 1.f, c, blockIdx.y == 0 && marked(p, a, s));
+        v.load(p, d.v, d.planes, s, tok, r, scale, c, blockIdx.y == 0 && marked(p, a, s));
         uint4* o = reinterpret_cast<uint4*>(d.ops + ((size_t)s * p.M + row) * (2 * p.r16));
         o[c] = v.half();
         o[chunks + c] = v.half();
@@ -1205,7 +1214,6 @@ expand_kernel(const OperandParams p)
         if (m * p.tile + row < p.M && (b < 0 || b >= t.count[row])) *piece_at(e, piece, row) = make_uint4(0u, 0u, 0u, 0u);
     }
     // this thread's eight ranks of a row and slice
-    static_assert(2 * kOpRows * (LORA_MAX_RANK / 8) <= kOpThreads, "a thread has one piece");
     const int chunks = p.r16 >> 3, c = tid % chunks, mine = tid / chunks, s = mine & 1, row = row0 + (mine >> 1), pos = m * p.tile + row;
     const bool live = mine < 2 * kOpRows && pos < p.M && (c >> 1) < t.count[row];
     int a = 0, tok = 0, r = 0;
@@ -1304,12 +1312,6 @@ int pair_count()
     return n > 0 ? n : 0;
 }
 
-struct GatedPlan {
-    bool pair;
-    int cols, mt, tiles, units;
-    int split;  // pieces of the last round's tiles, 1: they stay whole
-};
-
 // Whether the GEMM takes its tokens by adapter: where it saves a unit some rank blocks, if the batch is
 // mixed. Forward: six (the launch costs a sorted batch 1 us and the copy a mixed one 4: 300 tokens
 // of 5 adapters, three blocks saved, 30 us without, 34 with; 1024 tokens, seven saved, 66 and 58).
@@ -1346,12 +1348,14 @@ constexpr double kShareUs = 40;  // what pieces have to gain: accumulators go ou
 constexpr double kPieceUs = 1.2;  // and each more of a tile
 constexpr int kMaxSplit = 16, kPieces = 3;  // pieces of a tile; of all tiles per unit, at most
 
+}  // namespace
+
 // The cheapest choice: rounds of the units over the tiles, whole or with the last one shared. A
 // single token tile is bound by the weights' stream instead: there time per stage goes by bytes
 // (8192 x 28672, 16 tokens: 112 columns in two rounds 6.4 TB/s, 16 columns in thirteen 2 TB/s). A
 // pair's one tile is 256 tokens and half as many pairs share the stream (200 x 7424 x 8640: pairs,
 // which read the weights once, 53 us, single CTAs 61).
-GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
+GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save, const lora_pool_t* pool)
 {
     const int NC = bwd ? K : F, red = bwd ? 2 * ((F + 63) / 64) : (K + 63) / 64;
     const TileChoice* tiles = bwd ? kBwdTiles : kFwdTiles;
@@ -1386,10 +1390,9 @@ GatedPlan gated_plan(bool bwd, int M, int K, int F, bool save)
             best.units = (int)(split == 1 && all < units ? all : units);
         }
     }
+    best.by_adapter = pool && gated_order(best, bwd, M, pool->n_adapters, pool->r_max);
     return best;
 }
-
-}  // namespace
 
 // Room for the pieces of the backward's shared tiles, and for their counts.
 size_t gated_part_bytes() { return (size_t)device_sm_count() * kPieces * kGTileM * kGAccCols * 4; }
@@ -1451,18 +1454,12 @@ size_t gated_expand_bytes(int M, int n_adapters, int r_max)
     return most;
 }
 
-bool gated_by_adapter(bool backward, int M, const lora_pool_t& pool, bool save)
-{
-    return gated_order(gated_plan(backward, M, pool.h_in, pool.h_out, save), backward, M, pool.n_adapters, pool.r_max);
-}
-
 size_t gated_gather_bytes(int M, int K) { return M > kGTileM ? (size_t)M * K * 2 : 0; }
 
-cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
+cudaError_t launch_gated_gather(const GatedPlan& plan, const void* x, int M, int K, const lora_segments_t& seg, void* out,
                                 cudaStream_t stream)
 {
-    const int K = pool.h_in;
-    if (!gated_by_adapter(false, M, pool, save)) return cudaSuccess;
+    if (!plan.by_adapter) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((M + kGatherRows - 1) / kGatherRows), (unsigned)((K + kGatherCols - 1) / kGatherCols), 1);
     cfg.blockDim = dim3(kGatherThreads, 1, 1);
@@ -1475,10 +1472,9 @@ cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, c
     return cudaLaunchKernelEx(&cfg, gather_kernel, static_cast<const uint16_t*>(x), (const int32_t*)seg.perm, M, K, static_cast<uint16_t*>(out));
 }
 
-cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                  const uint8_t* bad, bool backward, bool save, void* lists, cudaStream_t stream)
+cudaError_t launch_gated_operands(const GatedPlan& plan, const GatedSide* sides, int n, int M, const lora_pool_t& pool,
+                                  const lora_segments_t& seg, const uint8_t* bad, bool backward, void* lists, cudaStream_t stream)
 {
-    const GatedPlan plan = gated_plan(backward, M, pool.h_in, pool.h_out, save);
     OperandParams p = {};
     p.tile = plan.pair ? 2 * kGTileM : kGTileM;
     for (int i = 0; i < n; ++i) {
@@ -1490,8 +1486,7 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     p.bad = bad;
     p.bad_parts = gated_scan_parts(sides[0].down, M, pool);
     p.tok_adapter = seg.tok_adapter;
-    const bool order = gated_order(plan, backward, M, pool.n_adapters, pool.r_max);
-    if (order) p.order = seg.perm;
+    if (plan.by_adapter) p.order = seg.perm;
     p.indptr = seg.indptr;
     p.ranks = pool.ranks;
     p.scales = pool.scales;
@@ -1505,7 +1500,7 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     if (!backward) {
         p.ups = gated_fwd_steps(plan, M).ups;
         p.rows = plan.pair ? 2 * kGTileM : gated_a_rows(M);
-        p.per_tile = order ? -1 : (int)(gated_steps(M, p.tile, p.ups, false, pool.n_adapters, pool.r_max) / plan.mt);
+        p.per_tile = plan.by_adapter ? -1 : (int)(gated_steps(M, p.tile, p.ups, false, pool.n_adapters, pool.r_max) / plan.mt);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.mt * (p.tile / kOpRows)), (unsigned)n, 1);
@@ -1519,14 +1514,13 @@ cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lo
     return backward ? cudaLaunchKernelEx(&cfg, operand_kernel, p) : cudaLaunchKernelEx(&cfg, expand_kernel, p);
 }
 
-cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
+cudaError_t launch_gated_gemm(const GatedPlan& plan, const GatedGemmArgs& a, cudaStream_t stream)
 {
     const bool bwd = a.backward;
     GatedParams p = {};
     p.M = a.M;
     p.NC = bwd ? a.K : a.F;
     const bool save = a.g8 != nullptr;
-    const GatedPlan plan = gated_plan(bwd, a.M, a.K, a.F, save);
     p.mt = plan.mt;
     p.cols = plan.cols;
     p.bn = bwd ? p.cols : 2 * p.cols;
@@ -1584,7 +1578,7 @@ cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream)
         p.list_len = p.lists + (size_t)p.mt * kListMax * (plan.pair ? 2 : 1);
         p.list_base = p.list_len + p.mt;
         p.tok_adapter = a.tok_adapter;
-        if (gated_order(plan, bwd, a.M, a.n_adapters, a.r_max)) p.order = a.order;
+        if (plan.by_adapter) p.order = a.order;
         p.n_adapters = a.n_adapters;
         p.r_max = a.r_max;
     }

@@ -70,7 +70,15 @@ cudaError_t launch_mxfp4_quantize(const void* W, int N, int K, uint8_t* Wp, uint
 cudaError_t launch_act8_compress(const void* x, int M, int N, const lora_act8_t& out, cudaStream_t stream);
 cudaError_t launch_act8_expand(const lora_act8_t& in, int M, int N, void* x, cudaStream_t stream);
 
-// The gated feed-forward block. launch_gated_operands turns the planes of v
+// The gated feed-forward block's GEMM for given sizes: its tiles, and whether its rows are the tokens in the
+// segments' order (with a pool; gated.cu says when).
+struct GatedPlan {
+    bool pair, by_adapter;
+    int cols, mt, tiles, units;
+    int split;  // pieces of the last round's tiles, 1: they stay whole
+};
+GatedPlan gated_plan(bool backward, int M, int K, int F, bool save, const lora_pool_t* pool);
+// launch_gated_operands turns the planes of v
 // [2][M][r_max] of each side into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
 // lists the rank blocks of each token tile of the GEMM that follows (backward or not, saving
 // checkpoints or not; gated_list_bytes). With adapters the launches
@@ -97,15 +105,15 @@ cudaError_t launch_gated_shrink(const GatedSide* sides, int n, int M, const lora
                                 uint8_t* bad, cudaStream_t stream);
 // Forward: the rows of x that the GEMM reads in the segments' order (gated.cu), before the shrink.
 size_t gated_gather_bytes(int M, int K);
-cudaError_t launch_gated_gather(const void* x, int M, const lora_pool_t& pool, const lora_segments_t& seg, bool save, void* out,
+cudaError_t launch_gated_gather(const GatedPlan& plan, const void* x, int M, int K, const lora_segments_t& seg, void* out,
                                 cudaStream_t stream);
 size_t gated_operand_bytes(int M, int r_max);
 size_t gated_expand_bytes(int M, int n_adapters, int r_max);
 size_t gated_list_bytes(int M);
 size_t gated_part_bytes();
 size_t gated_count_bytes();
-cudaError_t launch_gated_operands(const GatedSide* sides, int n, int M, const lora_pool_t& pool, const lora_segments_t& seg,
-                                  const uint8_t* bad, bool backward, bool save, void* lists, cudaStream_t stream);
+cudaError_t launch_gated_operands(const GatedPlan& plan, const GatedSide* sides, int n, int M, const lora_pool_t& pool,
+                                  const lora_segments_t& seg, const uint8_t* bad, bool backward, void* lists, cudaStream_t stream);
 struct GatedGemmArgs {
     bool backward;
     int M, K, F, act;
@@ -125,15 +133,13 @@ struct GatedGemmArgs {
     int n_adapters, r_max;
 };
 // cudaErrorInvalidValue if an operand's tensor map is refused.
-cudaError_t launch_gated_gemm(const GatedGemmArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_gemm(const GatedPlan& plan, const GatedGemmArgs& a, cudaStream_t stream);
 // dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu).
 // Also zeroes `count` (gated_count_bytes).
 // order: NULL, or the tokens of dg's and du's rows.
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
                                const int32_t* order, void* dg, void* du, void* h, int* count, cudaStream_t stream);
-// Whether the GEMM's rows are the tokens in the segments' order (gated.cu). by_adapter below: so are
-// d's and the operands'.
-bool gated_by_adapter(bool backward, int M, const lora_pool_t& pool, bool save);
+// by_adapter: the plan's.
 // Gradients of both slices, bf16: dA[s][a][k][j] = sum_t x[t][k] op_u[s][t][j] and dB[s][a][j][f] =
 // sum_t op_v[s][t][j] d[s][t][f] over the adapter's tokens.
 cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
