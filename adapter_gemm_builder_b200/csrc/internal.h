@@ -78,12 +78,11 @@ struct GatedPlan {
     int split;  // pieces of the last round's tiles, 1: they stay whole
 };
 GatedPlan gated_plan(bool backward, int M, int K, int F, bool save, const lora_pool_t* pool);
-// launch_gated_operands turns the planes of v
-// [2][M][r_max] of each side into the bf16 operands of s_a v (gated_operand_bytes: [2][M][hi r16 | lo r16]) and
-// lists the rank blocks of each token tile of the GEMM that follows (backward or not, saving
-// checkpoints or not; gated_list_bytes). With adapters the launches
-// right before launch_gated_gemm are a shrink that waits for its predecessors before it lets
-// its dependents start, then launch_gated_operands (gated.cu says why).
+// launch_gated_operands turns the planes of v [2][M][r_max] of each side into the bf16 operands of s_a v (backward:
+// gated_operand_bytes, [2][M][hi r16 | lo r16]; forward, one side: gated_expand_bytes, the GEMM's steps, see
+// expand_kernel) and lists the rank blocks of each token tile of the GEMM that follows (gated_list_bytes).
+// With adapters the launches right before launch_gated_gemm are a shrink that waits for its predecessors
+// before it lets its dependents start, then launch_gated_operands (gated.cu says why).
 // launch_gated_shrink, for each of n sides: gated_shrink_planes planes of v[s][t][j] = sum_l
 // lng[s][t][l] w, w = pool.A[s][a][l][j] (down: x.A) or pool.B[s][a][j][l] (else: d.B^T), lng_slice
 // 0: both slices read one lng (gated_grad.cu).
@@ -134,14 +133,13 @@ struct GatedGemmArgs {
 };
 // cudaErrorInvalidValue if an operand's tensor map is refused.
 cudaError_t launch_gated_gemm(const GatedPlan& plan, const GatedGemmArgs& a, cudaStream_t stream);
-// dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu).
-// Also zeroes `count` (gated_count_bytes).
-// order: NULL, or the tokens of dg's and du's rows.
+// dg, du (and h, may be NULL) from dh and the checkpoints of g and u (gated_grad.cu). Also zeroes `count`
+// (gated_count_bytes). order: NULL, or the tokens of dg's and du's rows.
 cudaError_t launch_gated_point(const void* dh, int M, int F, int act, const lora_act8_t& g8, const lora_act8_t& u8,
                                const int32_t* order, void* dg, void* du, void* h, int* count, cudaStream_t stream);
-// by_adapter: the plan's.
 // Gradients of both slices, bf16: dA[s][a][k][j] = sum_t x[t][k] op_u[s][t][j] and dB[s][a][j][f] =
-// sum_t op_v[s][t][j] d[s][t][f] over the adapter's tokens.
+// sum_t op_v[s][t][j] d[s][t][f] over the adapter's tokens. by_adapter: the plan's (the rows of d and of the
+// operands).
 cudaError_t launch_gated_outer(const void* x, const void* ops_u, void* dA, const void* d, const void* ops_v, void* dB, int M,
                                const lora_pool_t& pool, const lora_segments_t& seg, bool by_adapter, cudaStream_t stream);
 

@@ -474,8 +474,9 @@ LORA_API int act8_expand_rows(const lora_act8_t* in, int M, int N, void* x, lora
  *   ws: lora_workspace_size(LORA_OP_BF16_GATED, M, K, pool) bytes.
  * With adapters: the shrink (v = x.A, fp32), a small kernel that lists each token tile's
  * adapters and puts s_a v into bf16 halves hi + lo, then the GEMM as its programmatic
- * dependent; the term is part of the GEMM's sum. Its cost grows with the adapters per
- * 128 consecutive tokens, so batches sorted by adapter cost least. An adapter whose B (forward) or
+ * dependent; the term is part of the GEMM's sum. Batches of more than 128 tokens over many
+ * adapters are taken by adapter (x's rows copied first, unless they come as runs), so a mixed
+ * batch costs little more than one sorted by adapter. An adapter whose B (forward) or
  * A (backward) holds a non-finite value gives NaN to the whole rows of its own tokens (and to
  * its dA), and nothing to those of others.
  * h, g8 and u8 overlap neither each other nor an input; calls that may run at the same time have
