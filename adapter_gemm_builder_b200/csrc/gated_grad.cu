@@ -67,13 +67,6 @@ gated_point_kernel(const PointParams p)
         uint32_t gE[kEInFlight], uE[kEInFlight];
         size_t at[kEInFlight], to[kEInFlight];
         bool live[kEInFlight];
-        uint32_t tok[kEInFlight];
-#pragma unroll
-        for (int i = 0; i < kEInFlight; ++i) {
-            const uint64_t t = t0 + (uint64_t)i * stride;
-            tok[i] = t < p.tasks ? (uint32_t)t / p.segs : 0;
-            if (ORDER) tok[i] = (uint32_t)p.order[tok[i]];
-        }
 #pragma unroll
         for (int i = 0; i < kEInFlight; ++i) {
             const uint64_t t = t0 + (uint64_t)i * stride;
@@ -83,9 +76,10 @@ gated_point_kernel(const PointParams p)
                 const int col = (int)((uint32_t)t - row * p.segs) * kETaskCols + lane * 8;
                 if (col < p.F) {
                     live[i] = true;
+                    const uint32_t tok = ORDER ? (uint32_t)p.order[row] : row;
                     to[i] = (size_t)row * p.F + col;
-                    at[i] = (size_t)tok[i] * p.F + col;
-                    const size_t sc = (size_t)tok[i] * nb + (col >> 5);
+                    at[i] = (size_t)tok * p.F + col;
+                    const size_t sc = (size_t)tok * nb + (col >> 5);
                     dh[i] = __ldcs(reinterpret_cast<const uint4*>(p.dh + at[i]));
                     gc[i] = __ldcs(reinterpret_cast<const uint2*>(p.g_codes + at[i]));
                     uc[i] = __ldcs(reinterpret_cast<const uint2*>(p.u_codes + at[i]));
