@@ -1133,10 +1133,20 @@ struct Eight {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-            f[2 * e] -= bf16_lo(w[e]);
-            f[2 * e + 1] -= bf16_hi(w[e]);
+            f[2 * e] = rest(f[2 * e], w[e], 0);
+            f[2 * e + 1] = rest(f[2 * e + 1], w[e], 16);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // v less its half, the bf16 at `at` of w: nothing of an infinity or NaN, which the half holds (infinity less
+    // infinity would make NaN of it); a finite v that rounds to an infinity takes the largest bf16 as its half.
+    static __device__ __forceinline__ float rest(float v, uint32_t& w, int at)
+    {
+        if ((w >> at & 0x7f80u) == 0x7f80u) {
+            if (!act8::finite(v)) return 0.f;
+            w -= 1u << at;
+        }
+        return v - __uint_as_float(w >> at << 16);
     }
 };
 
