@@ -188,10 +188,14 @@ __device__ __forceinline__ bool wait_role(int id, int n, bool prober, uint64_t* 
 }
 
 // act(g): x sigmoid(x), or x Phi(x) through the complementary error function (no
-// cancellation in the lower tail).
+// cancellation in the lower tail). The sigmoid of exp(-|g|): with exp(-g) the denominator passes 2^126 below
+// g = -87, where the fast division gives zero.
 __device__ __forceinline__ float gate(int act, float g)
 {
-    if (act == LORA_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
+    if (act == LORA_ACT_SILU) {
+        const float t = __expf(-fabsf(g));
+        return __fdividef(g < 0.f ? g * t : g, 1.f + t);
+    }
     return 0.5f * g * erfcf(g * -0.70710678118654752f);
 }
 

@@ -37,14 +37,15 @@ struct PointParams {
     uint32_t tasks, segs;
 };
 
-// act(g) and act'(g).
+// act(g) and act'(g); the sigmoid of exp(-|g|), whose denominator stays within 2 (see gate in gated.cu).
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float g, float& a, float& d)
 {
     if (ACT == LORA_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + __expf(-g));
+        const float t = __expf(-fabsf(g)), big = __fdividef(1.f, 1.f + t), small = t * big;
+        const float s = g < 0.f ? small : big, rest = g < 0.f ? big : small;  // 1 - s
         a = g * s;
-        d = s * fmaf(g, 1.f - s, 1.f);
+        d = s * fmaf(g, rest, 1.f);
     } else {
         const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
         a = g * cdf;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from adapter_gemm_builder_b200 import lora as L
-from test_gpu_gated import FN, U, Problem, act64, backward, compress, forward, guarded, within
+from test_gpu_gated import FN, U, Problem, act64, backward, compress, forward, within
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,50 @@ def test_a_finite_v_past_the_largest_bf16(sign):
     want = torch.full((M, F), v * 2.0 ** -126, dtype=torch.float64) * act64("silu", torch.tensor(4.0, dtype=torch.float64))[0]
     # v's halves 2^-16, the activation, a rounding to bf16
     within(h, want, (2.0 ** -16 + FN + U) * 1.01 * want.abs(), "h")
+
+
+@pytest.mark.parametrize("save", [False, True])
+def test_silu_far_below_zero(save):
+    """silu(g) = g exp(g) / (1 + exp(g)) down to g = -88, where 1 + exp(-g) is past 2^126: the product with a
+    large u is an ordinary number. g = -k / 4 is a sum of one exact product, u = 2^100."""
+    K, F = 64, 32
+    M = 4 * 88 - 4 * 60
+    p = Problem(M, K, F, 0, 8, seed=24)
+    for z in (p.x, p.Wg, p.Wu):
+        z.zero_()
+    k = torch.arange(4 * 60, 4 * 88) + 1
+    p.x[:, 0], p.x[:, 1], p.x[:, 2] = -(k // 4).float(), -(k % 4).float() / 4, 2.0 ** 100
+    p.Wg[:, 0] = p.Wg[:, 1] = 1.0
+    p.Wu[:, 2] = 1.0
+    h, _ = forward(p, save=save)
+    g = (-k.double() / 4)[:, None].expand(M, F)
+    want = g * torch.exp(g) / (1 + torch.exp(g)) * 2.0 ** 100
+    # exp of the fast kind: 2 + 1.173 |g| units of 2^-23; then a product, a sum and a division
+    within(h, want, (U + 2.0 ** -23 * (2 + 1.173 * g.abs()) + 2.0 ** -20) * 1.01 * want.abs(), "h")
+
+
+def test_silu_gradient_far_below_zero():
+    """The same range in the backward: dg = dh u act'(g), du = dh act(g) through dX with a weight of one. g comes
+    from its checkpoint: -88 to -64 in steps of 8 are among its values exactly, and 2^60 times 2^40 keeps the
+    products in range."""
+    K, F = 16, 32
+    g = -torch.arange(64.0, 89.0, 8.0)
+    M = len(g)
+    p = Problem(M, K, F, 0, 8, seed=25)
+    p.Wg.zero_(), p.Wu.zero_()
+    p.Wg[0, 0], p.Wu[0, 8] = 1.0, 1.0
+    p.dh = torch.full((M, F), 2.0 ** 60).bfloat16()
+    g8, gv = compress(g[:, None].expand(M, F))
+    u8, uv = compress(torch.full((M, F), 2.0 ** 40))
+    assert (gv == g[:, None]).all() and (uv == 2.0 ** 40).all()
+    dX, h = torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), torch.empty(M, F, dtype=torch.bfloat16, device="cuda")
+    ws = L.workspace(L.LORA_OP_BF16_GATED_BACKWARD, M, F, None)
+    L.bf16_gated_lora_backward(p.dh.cuda(), p.Wg.cuda(), p.Wu.cuda(), None, None, g8, u8, None, dX, None, None, ws, h=h)
+    z = g.double()
+    e = torch.exp(z) / (1 + torch.exp(z))
+    act, slope = z * e, e * (1 + z * (1 - e))
+    rel = (2 * U + 2.0 ** -23 * (2 + 1.173 * 88) + 2.0 ** -19) * 1.01  # two roundings to bf16
+    dX, h = dX.cpu().double(), h.cpu().double()
+    for got, want, what in ((dX[:, 0], slope * 2.0 ** 100, "dg"), (dX[:, 8], act * 2.0 ** 60, "du"), (h[:, 0], act * 2.0 ** 40, "h")):
+        within(got, want, rel * want.abs(), what)
+    assert not dX[:, [1, 9]].any()
