@@ -305,6 +305,17 @@ int lora_debug_set_wait_limit(uint64_t limit_ns, int inject_stall)
     return LORA_OK;
 }
 
+int lora_debug_gated_plan(int backward, int M, int K, int F, int save, const lora_pool_t* pool, int32_t* plan)
+{
+    if (!plan || M < 1 || K < 8 || F < 8 || K % 8 || F % 8) return LORA_ERR_INVALID_ARG;
+    if (pool && (check_pool(pool) != LORA_OK || pool->n_slices != 2 || pool->h_in != K || pool->h_out != F))
+        return LORA_ERR_INVALID_ARG;
+    const GatedPlan p = gated_plan(backward != 0, M, K, F, save != 0, pool);
+    const int32_t out[7] = {p.pair, p.cols, p.mt, p.tiles, p.whole(), p.split, p.by_adapter};
+    for (int i = 0; i < 7; ++i) plan[i] = out[i];
+    return LORA_OK;
+}
+
 const char* lora_status_string(int s)
 {
     switch (s) {

@@ -1542,7 +1542,7 @@ cudaError_t launch_gated_gemm(const GatedPlan& plan, const GatedGemmArgs& a, cud
     p.units = plan.units;
     p.split = plan.split;
     p.rounds = plan.split > 1 ? plan.tiles / plan.units : (plan.tiles + plan.units - 1) / plan.units;
-    p.whole = plan.split > 1 ? p.rounds * plan.units : plan.tiles;
+    p.whole = plan.whole();
     p.shared = plan.tiles - p.whole;
     p.part = a.part;
     p.count = a.count;

@@ -76,6 +76,7 @@ struct GatedPlan {
     bool pair, by_adapter;
     int cols, mt, tiles, units;
     int split;  // pieces of the last round's tiles, 1: they stay whole
+    int whole() const { return split > 1 ? tiles / units * units : tiles; }  // tiles before the shared ones
 };
 GatedPlan gated_plan(bool backward, int M, int K, int F, bool save, const lora_pool_t* pool);
 // launch_gated_operands turns the planes of v [2][M][r_max] of each side into the bf16 operands of s_a v (backward:

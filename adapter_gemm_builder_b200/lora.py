@@ -46,7 +46,7 @@ EXPORTED = [
     "lora_noalloc_status", "lora_debug_set_wait_limit", "bf16_gemm_lora_epilogue",
     "lora_switch_merge", "fp8_lora_backward", "mxfp4_quantize_rows", "mxfp4_gemm_lora_epilogue",
     "w8a16_gemm_lora_epilogue", "act8_compress_rows", "act8_expand_rows",
-    "bf16_gated_gemm_lora_epilogue", "bf16_gated_lora_backward",
+    "bf16_gated_gemm_lora_epilogue", "bf16_gated_lora_backward", "lora_debug_gated_plan",
 ]
 
 
@@ -114,6 +114,7 @@ def load(path: str = LIB_PATH):
             "lora_noalloc_scratch_bytes": (Z, []),
             "lora_noalloc_status": (I, [P, P]),
             "lora_debug_set_wait_limit": (I, [ctypes.c_uint64, I]),
+            "lora_debug_gated_plan": (I, [I, I, I, I, I, P, P]),
             "bf16_gemm_lora_epilogue": (I, [P, I, I, I, P, P, P, P, P, Z, P]),
             "lora_switch_merge": (I, [P, I, I, P, P, P, I, P, P]),
             "fp8_lora_backward": (I, [P, P, I, I, I, P, P, P, P, P, P, P, P, Z, P]),
@@ -518,3 +519,10 @@ def lora_debug_set_wait_limit(limit_ns: int, inject_stall: bool = False) -> None
     """Test hook: limit of the kernels' bounded waits (0 = default 2 s) and the stall
     that makes one CTA of each later launch run out its wait."""
     _check(load().lora_debug_set_wait_limit(int(limit_ns), 1 if inject_stall else 0))
+
+
+def lora_debug_gated_plan(backward: bool, M: int, K: int, F: int, save: bool = False, pool: "Pool | None" = None) -> dict:
+    """Test hook: the gated block's tiles for these sizes on the current device."""
+    plan = (ctypes.c_int32 * 7)()
+    _check(load().lora_debug_gated_plan(int(backward), M, K, F, int(save), ctypes.byref(pool.c) if pool else None, plan))
+    return dict(zip(("pair", "columns", "token_tiles", "tiles", "whole_tiles", "pieces", "by_adapter"), plan))

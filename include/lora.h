@@ -551,12 +551,21 @@ LORA_API size_t lora_noalloc_scratch_bytes(void);
  * Test hook for the failure path (not for production use): limit_ns sets the
  * limit of every bounded device-side wait of later launches (1 us .. 2 s;
  * 0 restores the default of 2 s); inject_stall = 1 makes one CTA of each
- * later SGMV (non-decode tiles) and FP8 GEMM launch first wait on a barrier
+ * later SGMV (non-decode tiles), GEMM and gated GEMM launch first wait on a barrier
  * that nothing completes, so that wait runs out, the kernel takes its abort
  * path, returns, and the status calls report LORA_ERR_TIMEOUT. Process-wide;
  * LORA_ERR_INVALID_ARG for values outside those ranges.
  */
 LORA_API int lora_debug_set_wait_limit(uint64_t limit_ns, int inject_stall);
+
+/*
+ * Test hook: how the gated block's GEMM goes about these sizes on the current device, as the
+ * calls decide it (backward: its dX product; save, pool: as the forward is called).
+ * plan[0] pair of CTAs per tile, [1] output columns of a tile, [2] token tiles, [3] all tiles,
+ * [4] those kept whole, [5] pieces of each other tile (1: none is shared), [6] rows by adapter.
+ * LORA_ERR_INVALID_ARG for sizes or a pool that the calls refuse.
+ */
+LORA_API int lora_debug_gated_plan(int backward, int M, int K, int F, int save, const lora_pool_t* pool, int32_t* plan);
 
 /* Static string for a status code. */
 LORA_API const char* lora_status_string(int status);
