@@ -135,6 +135,26 @@ def test_backward_of_whole_numbers(M, K, F, n, r, way):
     check(p, out, room, args[-1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,F,n,r", [(70, 200, 272, 0, 8), (70, 200, 272, 5, 64), (100, 528, 8192, 0, 8), (100, 528, 8192, 16, 16),
+                                       (520, 264, 1040, 130, 32), (300, 528, 6000, 0, 8), (300, 528, 6000, 200, 32)])
+def test_a_wait_of_the_backward_runs_out(M, K, F, n, r):
+    """The bounded waits of the dX product (a CTA, a pair, shared tiles, with adapters and without): a launch
+    whose loads never begin on one CTA returns and reports it, and the next call on the same workspace is right."""
+    p = Whole(M, K, F, n, r)
+    args, out, room = p.arguments()
+    torch.cuda.synchronize()
+    L.lora_debug_set_wait_limit(1_000_000, inject_stall=True)
+    try:
+        L.bf16_gated_lora_backward(*args, act=L.LORA_ACT_GELU, h=out["h"])
+        torch.cuda.synchronize()
+    finally:
+        L.lora_debug_set_wait_limit(0, False)
+    assert L.lora_workspace_status(args[-1])[0] == L.LORA_ERR_TIMEOUT
+    L.bf16_gated_lora_backward(*args, act=L.LORA_ACT_GELU, h=out["h"])
+    check(p, out, room, args[-1])
+
+
 @pytest.mark.parametrize("M,K,F,n,r", [(70, 200, 272, 5, 64), (1, 128, 8192, 1, 16), (100, 528, 2048, 16, 16)])
 def test_the_whole_numbers_tell(M, K, F, n, r):
     """On the CPU: u to 8 bits, or 64 columns of the sum left out, is another dX after the rounding."""
