@@ -21,16 +21,17 @@
 // included, so that it is one or two boxes; B comes by TMA from the pool. The steps lie between the main
 // stages, in a unit's first tile in the last eighth, so that the shrink runs under the others.
 // (Steps of their own buffers, put together by eight warps with cp.async, had cost 1.5 us each where
-// they were many: 512 tokens of 48 adapters of rank 32 388 us, 171 in the ring.)
+// they were many: 512 tokens sorted over 48 adapters of rank 32, 4096 x 11008, 388 us, 171 in the ring.)
 // Backward: a step has shared memory beside the ring, where builders put it together with cp.async, one
 // ahead of the one that they hand over where two buffers fit; its sums are long beside its steps.
 // The tokens of more than one token tile come in the segments' order, by adapter, where that saves
 // steps (gated_order): a tile then needs few adapters' blocks however the batch is mixed. gather_kernel
 // copies x's rows into that order, except where 128 of them follow one another already, as in a
-// batch that comes sorted; h and the checkpoints are written to the tokens' own rows. (2048 tokens
-// mixed over 48 adapters of rank 16: 940 us in their own order, 298 in this; over 16 of rank 64 1480,
-// 336. TMA's gather of four rows at a time took 1.2 us a stage instead of .4.) The backward
-// writes dg and du in that order to begin with.
+// batch that comes sorted; h and the checkpoints are written to the tokens' own rows. (4096 x 11008, 2048
+// tokens mixed over 48 adapters of rank 16: 940 us in their own order, 301 in this; over 16 of rank 64 1480,
+// 329; 20 calls in a row, called for seconds the latter are 343 and 371, by the power cap. TMA's gather of
+// four rows at a time took 1.2 us a stage instead of .4.) The backward writes dg and du in that order to
+// begin with.
 //
 // More than 128 tokens usually run on pairs of CTAs (cta_group::2, clusters of two): 256 tokens by
 // the same columns, each CTA with its 128 rows of A and half of B (forward: the even CTA the
@@ -268,8 +269,8 @@ constexpr int kNoBlock = -3 * 512;  // an adapter that no row has, nothing live
 // rows must not reach past the rank, where the pool holds anything, so the last block of several is the
 // last 16 ranks, and a single one below 16 is its first p and its last p ranks, p the largest power of
 // two, zeros behind them. What comes twice is used once. (Boxes of the powers of two that make up the
-// rank, and zeros to 16, five or six copies: 512 tokens of 48 adapters of rank up to 32 139 us, so 135; 36
-// of 32 53.6, 52.)
+// rank, and zeros to 16, five or six copies: side by side, 4096 x 11008, 512 tokens of 48 adapters of ranks drawn up
+// to 32 139 us, so 135; 36 of 32 53.6, 52.)
 __device__ __forceinline__ int block_rank(int R, int b, int j)
 {
     if (R >= 16) {
@@ -1016,7 +1017,7 @@ struct OperandParams {
     int bad_parts;
     int tile;  // tokens a list covers: 128 or 256
     int32_t *lists, *list_len, *list_base;
-    // forward: the GEMM's steps, see GatedSteps
+    // forward: the GEMM's steps, see FwdSteps
     int ups, rows, per_tile;
 };
 
@@ -1358,7 +1359,10 @@ constexpr TileChoice kBwdTiles[] = {{true, 256, .42}, {true, 128, .357}, {false,
 // forward: pairs 275 us, single CTAs 332; backward 512 x 1024 x 5216: 39 and 52). On aligned rows
 // the pair is ahead where the table calls it even (937 x 6144 x 9952: 165 us, 174).
 constexpr double kSingleCost = 1.03, kSingleSplitRows = 1.3;
-constexpr double kShareUs = 40;  // what pieces have to gain: accumulators go out and in, the tail is longer
+// What pieces have to gain: accumulators go out and in, the tail is longer. Found on 4096 x 11008,
+// it does not scale with the tile or the pieces, so a product that takes less than this is never shared
+// (333 tokens, 1040 x 2768: 18 pairs of 74 at work for 29 us).
+constexpr double kShareUs = 40;
 constexpr double kPieceUs = 1.2;  // and each more of a tile
 constexpr int kMaxSplit = 16, kPieces = 3;  // pieces of a tile; of all tiles per unit, at most
 

@@ -471,14 +471,19 @@ LORA_API int act8_expand_rows(const lora_act8_t* in, int M, int N, void* x, lora
  *   x bf16 [M][K]; Wg, Wu bf16 [F][K]; h bf16 [M][F] (out).
  *   pool: NULL, or n_slices == 2 (slice 0 the gate's adapters, slice 1 up's), h_in == K,
  *   h_out == F. seg: required when pool != NULL (built for these M tokens).
- *   ws: lora_workspace_size(LORA_OP_BF16_GATED, M, K, pool) bytes.
+ *   ws: lora_workspace_size(LORA_OP_BF16_GATED, M, K, pool) bytes. With adapters it holds, beside v and for
+ *   M > 128 x's rows, the term's operand written out: 128 bytes per token row of a tile (128 or 256 tokens) and
+ *   rank block (16 ranks of an adapter) that the tile may use. That goes by the pool's adapters, not the batch's:
+ *   8192 tokens take 79 MB of workspace with 8 adapters of r_max 16 and 86 MB with 64 (h_in 4096), 1024 tokens
+ *   with a pool of 1024 adapters of r_max 64 take 144 MB (h_in 4096).
  * With adapters: the shrink (v = x.A, fp32), a small kernel that lists each token tile's
  * adapters and puts s_a v into bf16 halves hi + lo, then the GEMM as its programmatic
  * dependent; the term is part of the GEMM's sum. Batches of more than 128 tokens over many
  * adapters are taken by adapter (x's rows copied first, unless they come as runs), so a mixed
  * batch costs little more than one sorted by adapter. An adapter whose B (forward) or
  * A (backward) holds a non-finite value gives NaN to the whole rows of its own tokens (and to
- * its dA), and nothing to those of others.
+ * its dA), and nothing to those of others. Any other infinity (in x, in A in the forward, in B in the
+ * backward, or an overflow of v) gives what the formula gives.
  * h, g8 and u8 overlap neither each other nor an input; calls that may run at the same time have
  * a workspace each.
  * Limits: M >= 1, K % 8 == 0, F % 8 == 0, F % 16 == 0 with checkpoints.
